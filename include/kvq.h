@@ -78,6 +78,12 @@ typedef enum kvq_format {
     KVQ_FP8_E4M3 = 2    /* FP8 E4M3, scale = absmax / 448 per (page, head) */
 } kvq_format;
 
+/* element type of original (unquantized) rows; the cache's own entry points take fp16 */
+typedef enum kvq_dtype {
+    KVQ_FP16 = 0, /* IEEE binary16 */
+    KVQ_BF16 = 1  /* bfloat16 */
+} kvq_dtype;
+
 /* bits of the device status word */
 #define KVQ_FLAG_BAD_PAGE 0x1    /* a block-table entry was out of range (that page was not touched) */
 #define KVQ_FLAG_BAD_LENGTH 0x2  /* a sequence length exceeded max_blocks_per_seq * 64 */
@@ -311,6 +317,116 @@ kvq_status kvq_prefill_attention(const kvq_cache *cache, const uint16_t *q, int3
  * shape.
  */
 size_t kvq_prefill_workspace_bytes(int32_t num_q_heads, int32_t num_seqs, int32_t max_q_per_seq);
+
+/*
+ * kvq_prompt_attention -- causal attention of whole prompts over their own
+ * rows, before (or while) kvq_append quantizes them (dynamic chunked attention
+ * of new tokens: "R1 performance overview", aicoding.csdn.net).  Sequence b's
+ * rows are cu_seqlens[b] .. cu_seqlens[b+1]-1 of q, k and v; for its token i
+ * and query head hq, over cache head hq / g (g = num_q_heads / num_kv_heads):
+ *   out[row][hq][:] = sum_{t <= i} softmax_t(softmax_scale q_i . k_t) v_t
+ *   lse[row][hq]    = ln sum_{t <= i} exp(softmax_scale q_i . k_t)
+ * on the tensor cores (tcgen05): operands of type dtype, binary32 scores,
+ * statistics and accumulation, probabilities rounded to dtype as the PV
+ * operand.  Any finite softmax_scale.  Values of v that are not finite reach
+ * the rows that attend to them and no others; rows of q, k and v outside every
+ * sequence may hold anything, and out and lse are left as they were there.
+ *   q                [total_tokens][num_q_heads][head_dim], row r at element
+ *                    r * q_row_stride; k, v likewise with num_kv_heads (views
+ *                    into one fused projection's rows, for instance).  Strides
+ *                    are multiples of 8 elements, at least a row; 16-byte
+ *                    aligned
+ *   out              [total_tokens][num_q_heads][head_dim], no gaps, 16-byte aligned
+ *   lse              binary32 [total_tokens][num_q_heads], or NULL
+ *   cu_seqlens       device int32 [num_seqs + 1], non-decreasing, cu[0] >= 0
+ *   max_tokens_per_seq  host bound on every length; 0 is a no-op
+ *   status           one int32 for KVQ_FLAG_* bits (the cache's status word,
+ *                    for instance), or NULL
+ * A sequence that breaks a bound is skipped and KVQ_FLAG_BAD_LENGTH set.
+ * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (head_dim != 128, unknown
+ * dtype, g > 128, more than 65535 sequences, total_tokens above 2^31 - 1),
+ * KVQ_ERR_CUDA.
+ */
+kvq_status kvq_prompt_attention(kvq_dtype dtype, const uint16_t *q, int64_t q_row_stride, const uint16_t *k,
+                                int64_t k_row_stride, const uint16_t *v, int64_t v_row_stride, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, const int32_t *cu_seqlens,
+                                int64_t total_tokens, int32_t max_tokens_per_seq, int32_t num_seqs,
+                                float softmax_scale, uint16_t *out, float *lse, int32_t *status,
+                                kvq_stream_t stream);
+
+/*
+ * kvq_page_weights -- the softmax weight that each page of the cache receives
+ * from the newest queries of its sequence, added to a running total: what
+ * kvq_evict_pages goes by.  The queries are laid out as in
+ * kvq_prefill_attention: n_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] rows, query
+ * i at position p_i = seq_lens[b] - n_b + i (n_b = 1 in a decode step, the last
+ * tokens of a prompt before its first answer token).  For page j < nb =
+ * ceil(seq_lens[b] / 64):
+ *   weights_out[b][j] = decay * weights_in[b][j]
+ *     + sum_{i, hq} sum_{t in page j, t <= p_i} softmax_t(softmax_scale q_i,hq . k^_t)
+ * so the new weights of a sequence sum to n_b * num_q_heads.  Entries from nb
+ * on are written as 0; a sequence without new queries keeps its weights (no
+ * decay).  Only the keys are read.  Equal inputs give equal bits.
+ *   q                fp16 [total_q][num_q_heads][head_dim], 16-byte aligned;
+ *                    query head hq reads cache head hq / g
+ *   weights_in       binary32 [num_seqs][max_blocks_per_seq], or NULL for zeros
+ *   weights_out      binary32 [num_seqs][max_blocks_per_seq]; may be weights_in
+ *   decay            any finite factor; 1 accumulates, less lets old weight fade
+ *   workspace        >= kvq_page_weights_workspace_bytes(...) bytes, 16-byte
+ *                    aligned, any contents.  Do not share one workspace
+ *                    between calls that may run concurrently.
+ * A sequence that breaks a bound is skipped (its row stays as it was) and
+ * KVQ_FLAG_BAD_LENGTH set; a block-table entry out of range sets
+ * KVQ_FLAG_BAD_PAGE (page 0 is read instead).  Errors: KVQ_ERR_INVALID_ARG,
+ * KVQ_ERR_UNSUPPORTED (also max_blocks_per_seq above 2^22, or 2^30 or more
+ * query rows of one sequence and cache head), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
+ */
+kvq_status kvq_page_weights(const kvq_cache *cache, const uint16_t *q, int32_t num_q_heads,
+                            const int32_t *cu_seqlens_q, int64_t total_q, int32_t max_q_per_seq,
+                            const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                            int32_t num_seqs, float softmax_scale, float decay, const float *weights_in,
+                            float *weights_out, void *workspace, size_t workspace_bytes, kvq_stream_t stream);
+
+/*
+ * kvq_page_weights_workspace_bytes -- bytes of kvq_page_weights' workspace
+ * (one binary32 per query row, head and block); 0 for arguments that are not
+ * positive.
+ */
+size_t kvq_page_weights_workspace_bytes(int64_t total_q, int32_t num_q_heads, int32_t max_blocks_per_seq);
+
+/*
+ * kvq_evict_pages -- let the pages of least weight leave each sequence's block
+ * table.  A page is what the table addresses and what shares a scale, so whole
+ * pages go, for all heads; no code is read, moved or re-quantized.  Of the nb =
+ * ceil(seq_lens[b] / 64) pages of sequence b the first sink_blocks and the last
+ * max(recent_blocks, 1) always stay (so the open page does, and the fp16 tail
+ * rows stay valid); of the others those of largest weight stay until
+ * keep_blocks[b] pages do, ties to the lower index (a NaN counts as the least
+ * weight).  Then
+ *   table_out[b]    = kept pages in order, then the entries from nb on (pages
+ *                     reserved for growth, if any), then the evicted pages in
+ *                     order: a permutation of block_table[b], whose last
+ *                     num_evicted[b] entries the caller may give to others
+ *   seq_lens_out[b] = seq_lens[b] - 64 * num_evicted[b]
+ *   weights_out[b]  = the kept pages' weights, then zeros
+ * Every later call takes the shorter sequence as it is (append continues its
+ * open page; causal attention counts positions within it).  Positions that were
+ * rotated into the keys before they were cached stay the original ones: count
+ * new tokens' positions apart from seq_lens.
+ *   block_table, table_out    device int32 [num_seqs][max_blocks_per_seq]
+ *   seq_lens, seq_lens_out    device int32 [num_seqs]
+ *   weights, weights_out      binary32 [num_seqs][max_blocks_per_seq]
+ *   keep_blocks, num_evicted  device int32 [num_seqs]
+ *   status                    one int32 for KVQ_FLAG_* bits, or NULL
+ * Each output may be its input (not another's input or output).  A sequence
+ * whose length breaks a bound is copied unchanged, with num_evicted 0, and
+ * KVQ_FLAG_BAD_LENGTH set.  Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED
+ * (max_blocks_per_seq above 24576: a row is held on one SM), KVQ_ERR_CUDA.
+ */
+kvq_status kvq_evict_pages(const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                           const float *weights, int32_t num_seqs, const int32_t *keep_blocks, int32_t sink_blocks,
+                           int32_t recent_blocks, int32_t *table_out, int32_t *seq_lens_out, float *weights_out,
+                           int32_t *num_evicted, int32_t *status, kvq_stream_t stream);
 
 /*
  * Decode step as a CUDA graph (CUDA Graph instance reuse: "hardware-aware

@@ -49,7 +49,7 @@ def _stale(target, deps):
 
 
 def _headers():
-    return (glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) +
+    return (glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) +
             glob.glob(os.path.join(SYNTH, "*.h")))
 
 

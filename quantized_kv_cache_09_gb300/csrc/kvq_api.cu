@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "kvq.h"
+#include "kvq_around.h"
 #include "kvq_internal.h"
 #include "kvq_testing.h"
 
@@ -259,6 +260,135 @@ kvq_status kvq_prefill_attention(const kvq_cache *cache, const uint16_t *q, int3
         p.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + (counters + 255) / 256 * 256);
     }
     return from_cuda(kvq::launch_prefill(cache->fmt, p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvq_status kvq_prompt_attention(kvq_dtype dtype, const uint16_t *q, int64_t q_row_stride, const uint16_t *k,
+                                int64_t k_row_stride, const uint16_t *v, int64_t v_row_stride, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, const int32_t *cu_seqlens,
+                                int64_t total_tokens, int32_t max_tokens_per_seq, int32_t num_seqs,
+                                float softmax_scale, uint16_t *out, float *lse, int32_t *status,
+                                kvq_stream_t stream)
+{
+    if ((dtype != KVQ_FP16 && dtype != KVQ_BF16) || head_dim != kvq::kHeadDim) return KVQ_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || max_tokens_per_seq < 0 || total_tokens < 0 || !isfinite(softmax_scale))
+        return KVQ_ERR_INVALID_ARG;
+    if (num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads) return KVQ_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)num_q_heads * head_dim, kv_row = (int64_t)num_kv_heads * head_dim;
+    if (q_row_stride < q_row || k_row_stride < kv_row || v_row_stride < kv_row) return KVQ_ERR_INVALID_ARG;
+    if (q_row_stride % 8 || k_row_stride % 8 || v_row_stride % 8) return KVQ_ERR_INVALID_ARG;
+    const int g = num_q_heads / num_kv_heads;
+    if (g > kvq::kMaxPromptGroup || num_seqs > 65535 || total_tokens > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+    // a row's bytes are a 40-bit stride of a tensor map
+    const int64_t widest = q_row_stride > k_row_stride ? q_row_stride : k_row_stride;
+    if ((widest > v_row_stride ? widest : v_row_stride) >= (int64_t)1 << 39) return KVQ_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_tokens_per_seq == 0 || total_tokens == 0) return KVQ_OK;
+    if (!q || !k || !v || !out || !cu_seqlens) return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return KVQ_ERR_INVALID_ARG;
+    kvq::PromptParams p;
+    p.cu = cu_seqlens;
+    p.out = out;
+    p.lse = lse;
+    p.v = v;
+    p.v_stride = v_row_stride;
+    p.status = status;
+    p.num_seqs = num_seqs;
+    p.num_heads = num_kv_heads;
+    p.num_q_heads = num_q_heads;
+    p.group = g;
+    p.max_n = max_tokens_per_seq;
+    p.total = total_tokens;
+    p.score_scale = softmax_scale * 1.4426950408889634f;
+    p.tile_tokens = 128 / g;
+    return from_cuda(kvq::launch_prompt(dtype, p, q, q_row_stride, k, k_row_stride, device_sms(),
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t kvq_page_weights_workspace_bytes(int64_t total_q, int32_t num_q_heads, int32_t max_blocks_per_seq)
+{
+    if (total_q <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0) return 0;
+    return kvq::page_weights_workspace_bytes(total_q, num_q_heads, max_blocks_per_seq);
+}
+
+kvq_status kvq_page_weights(const kvq_cache *cache, const uint16_t *q, int32_t num_q_heads,
+                            const int32_t *cu_seqlens_q, int64_t total_q, int32_t max_q_per_seq,
+                            const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                            int32_t num_seqs, float softmax_scale, float decay, const float *weights_in,
+                            float *weights_out, void *workspace, size_t workspace_bytes, kvq_stream_t stream)
+{
+    kvq_status st = check_cache(cache);
+    if (st != KVQ_OK) return st;
+    if (num_seqs < 0 || max_q_per_seq < 0 || total_q < 0 || max_blocks_per_seq <= 0 || !isfinite(softmax_scale) ||
+        !isfinite(decay))
+        return KVQ_ERR_INVALID_ARG;
+    if (num_q_heads <= 0 || num_q_heads % cache->num_heads) return KVQ_ERR_INVALID_ARG;
+    const int g = num_q_heads / cache->num_heads;
+    if (max_blocks_per_seq > (1 << 22) || (int64_t)max_q_per_seq * g >= (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return KVQ_OK;
+    if (!cu_seqlens_q || !block_table || !seq_lens || !weights_out) return KVQ_ERR_INVALID_ARG;
+    if (total_q > 0 && max_q_per_seq > 0) {
+        if (!q || !aligned16(q)) return KVQ_ERR_INVALID_ARG;
+        if (!workspace || !aligned16(workspace) ||
+            workspace_bytes < kvq::page_weights_workspace_bytes(total_q, num_q_heads, max_blocks_per_seq))
+            return KVQ_ERR_WORKSPACE;
+    }
+    kvq::PageWeightsParams p;
+    p.k_codes = cache->k_codes;
+    p.k_scales = cache->k_scales;
+    p.q = q;
+    p.status = cache->status;
+    p.num_heads = cache->num_heads;
+    p.num_q_heads = num_q_heads;
+    p.group = g;
+    p.num_pages = cache->num_pages;
+    p.max_blocks = max_blocks_per_seq;
+    p.max_q = max_q_per_seq;
+    p.total_q = total_q;
+    p.score_scale = softmax_scale * 1.4426950408889634f;
+    p.decay = decay;
+    p.lse = static_cast<float *>(workspace);
+    p.part = p.lse + kvq::page_weights_lse_floats(total_q, num_q_heads, max_blocks_per_seq);
+    const int sms = device_sms();
+    if (sms <= 0) return KVQ_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    for (int32_t b0 = 0; b0 < num_seqs; b0 += kvq::kMaxSeqsPerLaunch) {
+        const int64_t row = (int64_t)b0 * max_blocks_per_seq;
+        p.num_seqs = (num_seqs - b0) < kvq::kMaxSeqsPerLaunch ? (num_seqs - b0) : kvq::kMaxSeqsPerLaunch;
+        p.cu_q = cu_seqlens_q + b0;
+        p.seq_lens = seq_lens + b0;
+        p.block_table = block_table + row;
+        p.weights_in = weights_in ? weights_in + row : nullptr;
+        p.weights_out = weights_out + row;
+        if (kvq::launch_page_weights(cache->fmt, p, sms, s) != cudaSuccess) return KVQ_ERR_CUDA;
+    }
+    return KVQ_OK;
+}
+
+kvq_status kvq_evict_pages(const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                           const float *weights, int32_t num_seqs, const int32_t *keep_blocks, int32_t sink_blocks,
+                           int32_t recent_blocks, int32_t *table_out, int32_t *seq_lens_out, float *weights_out,
+                           int32_t *num_evicted, int32_t *status, kvq_stream_t stream)
+{
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || sink_blocks < 0 || recent_blocks < 0) return KVQ_ERR_INVALID_ARG;
+    if (max_blocks_per_seq > kvq::kMaxEvictBlocks) return KVQ_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return KVQ_OK;
+    if (!block_table || !seq_lens || !weights || !keep_blocks || !table_out || !seq_lens_out || !weights_out ||
+        !num_evicted)
+        return KVQ_ERR_INVALID_ARG;
+    kvq::EvictParams p;
+    p.table = block_table;
+    p.seq_lens = seq_lens;
+    p.weights = weights;
+    p.keep = keep_blocks;
+    p.table_out = table_out;
+    p.seq_lens_out = seq_lens_out;
+    p.weights_out = weights_out;
+    p.num_evicted = num_evicted;
+    p.status = status;
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.sink = sink_blocks;
+    p.recent = recent_blocks;
+    return from_cuda(kvq::launch_evict(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kvq_status kvq_get_device_status(const kvq_cache *cache, kvq_stream_t stream, int32_t *flags_out)

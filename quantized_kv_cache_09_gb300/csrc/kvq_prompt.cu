@@ -1,0 +1,734 @@
+// kvq_prompt.cu -- causal attention of whole prompts over their own fp16 or
+// bf16 rows: packed sequences of different lengths, grouped query heads.  What
+// a first prompt runs beside kvq_append, which quantizes the same rows (dynamic
+// chunked attention, "R1 performance overview", aicoding.csdn.net; grouped
+// heads as for decode, ddd.cn section 2).
+//
+//   out_i = sum_{t <= i} softmax_t(scale q_i . k_t) v_t,  lse_i = ln sum_{t <= i} e^(scale q_i . k_t)
+//
+// Bound by the tensor cores (4 * 128 flops per query head and key, every byte
+// read about once from HBM): tcgen05 with S, P and O in tensor memory, operands
+// brought by TMA.  One CTA per SM stays resident and takes units in turn; a unit
+// is two tiles of 128 query rows of one (sequence, cache head).  A tile's rows
+// are tile_tokens = 128 / g tokens x the g query heads of the group (row = token
+// * g + head), so that a group of any size reads its cache head's keys once and
+// short prompts fill the tile with heads.  Keys go in steps of 128.
+//
+// Roles (warps), handing over through mbarriers:
+//   0-3, 4-7  softmax of tile 0, tile 1: one thread per query row.  A row of S
+//             (128 scores) is read into registers once; maximum, 2^(s - m), the
+//             row sum in binary32; P rounded to the operands' type (the tensor
+//             cores take nothing wider) goes over S in two halves.  The running
+//             maximum is lazy: O is rescaled only when a row's maximum grows by
+//             more than 2^8, so P stays in [0, 256].
+//   8-11      the last step(s) of a unit hold keys past some row's position:
+//             their V rows past the sequence's end are zeroed and values that
+//             are not finite taken out (0 * inf would reach rows that do not see
+//             them; the epilogue adds them to the rows that do).  Then the
+//             epilogue: O / l, while the tensor cores are on the next unit.
+//   12        issues the MMAs (one thread): S = Q K^T, O += P V, M = N = 128.
+//   13        walks the unit list and issues the TMA copies: Q tiles and a ring
+//             of five 32 KB stages, K and V alternating.
+// While one tile's rows are in the softmax, the tensor cores work on the other.
+//
+// Unit order: by the number of the unit in its sequence, the highest (most
+// keys) first, over sequences and cache heads, dealt to the CTAs forwards and
+// backwards in turn -- longest first without a counter to fetch from.
+#include <cuda.h>
+
+#include "kvq_around.h"
+#include "kvq_device.cuh"
+#include "kvq_internal.h"
+#include "kvq_tc.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr int kUnitTiles = 2;
+constexpr int kKeys = 128;
+constexpr int kStages = 5;
+constexpr int kTileBytes = kTileRows * kHeadDim * 2;
+constexpr int kPromptThreads = 512;
+constexpr uint32_t kPromptTmem = 512;  // tile t: S / P at columns 256 t, O at 256 t + 128
+constexpr float kLazy = 8.0f;
+constexpr float kLn2 = 0.693147180559945309f;
+// a softmax scale of 0 scores 1e-38 * raw instead, so that a masked score stays -inf
+constexpr float kMinScale = 1.17549435e-38f;
+// registers per thread after the split: 2 * 176 + 104 + 56 = 4 * 128, the launch's
+constexpr int kRegsSoftmax = 176, kRegsEpilogue = 104, kRegsIssue = 56;
+static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsIssue <= 4 * (65536 / kPromptThreads), "register split");
+
+// 16-bit element type: fp16 or bf16
+template <bool BF>
+struct Elem {
+    // f32 += a x b, M = 128, N = 128, K-major A and B (PV: B MN-major)
+    static constexpr uint32_t kIdescS =
+        (1u << 4) | (BF ? (1u << 7) | (1u << 10) : 0u) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    static constexpr uint32_t kIdescO = kIdescS | (1u << 16);
+    static constexpr uint32_t kExp = BF ? 0x7F807F80u : 0x7C007C00u;  // exponent bits of a pair
+    static constexpr uint32_t kOne = BF ? 0x00800080u : 0x04000400u;  // their last
+    __device__ static __forceinline__ uint32_t pack(float a, float b)
+    {
+        if constexpr (BF) {
+            uint32_t d;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+            return d;
+        } else {
+            return f16x2_rn(a, b);
+        }
+    }
+    // bit 15 / 31 set where the pair's low / high value is not finite
+    __device__ static __forceinline__ uint32_t wild(uint32_t w) { return ((w & kExp) + kOne) & 0x80008000u; }
+    __device__ static __forceinline__ float value(uint16_t x)
+    {
+        if constexpr (BF)
+            return __uint_as_float((uint32_t)x << 16);
+        else
+            return __half2float(__ushort_as_half(x));
+    }
+};
+
+struct PromptUnit {
+    int32_t c0, n, h, tok0;  // first row and length of the sequence, cache head, first token; n < 0: no more units
+};
+
+struct alignas(1024) PromptSmem {
+    uint8_t q[kUnitTiles][kTileBytes];
+    uint8_t kv[kStages][kTileBytes];
+    uint64_t kv_full[kStages];   // a stage's copy done: K, or V of a step without masked keys
+    uint64_t kv_raw[kStages];    // the same for V of a mixed step (then kv_clean)
+    uint64_t kv_clean[kStages];  // that V cleaned
+    uint64_t kv_free[kStages];   // the MMAs that read the stage complete
+    uint64_t q_full[kUnitTiles], q_free[kUnitTiles];
+    uint64_t s_full[kUnitTiles];   // S of a step complete, and every MMA before it
+    uint64_t p_half[kUnitTiles];   // P of keys 0..63 in tensor memory, O rescaled
+    uint64_t p_full[kUnitTiles];   // P of keys 64..127
+    uint64_t o_full[kUnitTiles];   // a unit's last PV complete
+    uint64_t o_free[kUnitTiles];   // O and ml read by the epilogue
+    uint64_t ml_full[kUnitTiles];  // a unit's maxima and sums written
+    uint64_t unit_full[2], unit_free[2];
+    uint64_t mma_done;
+    float2 ml[kUnitTiles][kTileRows];
+    PromptUnit unit[2];
+    uint32_t tmem;
+};
+static_assert(sizeof(PromptSmem) <= 227 * 1024, "one CTA's shared memory");
+
+// what a unit spans, from its record
+struct Span {
+    int active;             // tiles with a token
+    int steps[kUnitTiles];  // key steps of a tile
+    int total;              // of the unit
+    int mixed;              // first step with keys past some row's position
+    __device__ __forceinline__ Span(const PromptUnit &u, int tile_tokens)
+    {
+        active = u.n - u.tok0 > tile_tokens ? 2 : 1;
+        steps[0] = (min(u.tok0 + tile_tokens, u.n) - 1) / kKeys + 1;
+        steps[1] = active == 2 ? (min(u.tok0 + 2 * tile_tokens, u.n) - 1) / kKeys + 1 : 0;
+        total = max(steps[0], steps[1]);
+        mixed = (u.tok0 + 1) / kKeys;
+    }
+};
+
+// a position in the ring of stages
+struct Ring {
+    uint32_t stage = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// barrier 1 over the four epilogue warps, returning whether any thread passed `v`
+__device__ __forceinline__ bool epilogue_any(bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+}  // namespace
+
+template <bool BF>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    prompt_attn_kernel(PromptParams p, const __grid_constant__ CUtensorMap map_q,
+                       const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+{
+    using E = Elem<BF>;
+    extern __shared__ __align__(1024) uint8_t smem_prompt[];
+    PromptSmem &sm = *reinterpret_cast<PromptSmem *>(smem_prompt);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.group, tt = p.tile_tokens;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; s++) {
+            mbar_init(&sm.kv_full[s], 1);
+            mbar_init(&sm.kv_free[s], 1);
+            mbar_init(&sm.kv_raw[s], 1);
+            mbar_init(&sm.kv_clean[s], 4);
+        }
+        for (int t = 0; t < kUnitTiles; t++) {
+            mbar_init(&sm.q_full[t], 1);
+            mbar_init(&sm.q_free[t], 1);
+            mbar_init(&sm.s_full[t], 1);
+            mbar_init(&sm.p_half[t], 4);
+            mbar_init(&sm.p_full[t], 4);
+            mbar_init(&sm.o_full[t], 1);
+            mbar_init(&sm.o_free[t], 4);
+            mbar_init(&sm.ml_full[t], 4);
+        }
+        for (int s = 0; s < 2; s++) {
+            mbar_init(&sm.unit_full[s], 1);
+            mbar_init(&sm.unit_free[s], 13);  // 8 softmax warps, 4 epilogue warps, the MMA thread
+        }
+        mbar_init(&sm.mma_done, 1);
+        mbar_init_fence();
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)),
+                     "r"(kPromptTmem));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    bool ok = true;
+
+    // the r-th unit of this CTA, for every role but the loader's
+    auto fetch = [&](int r, PromptUnit &u) {
+        ok = mbar_wait_bounded(&sm.unit_full[r & 1], (uint32_t)(r >> 1) & 1u);
+        if (ok) u = sm.unit[r & 1];
+        return ok;
+    };
+
+    if (warp < 8) {
+        // ---- softmax: tile t, one query row per thread (its lane of tensor memory) ----
+        regs_inc<kRegsSoftmax>();
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t tm = tmem + 256u * t + ((uint32_t)((warp & 3) * 32) << 16);
+        const float sabs = fmaxf(fabsf(p.score_scale), kMinScale);
+        const bool neg = p.score_scale < 0.0f;
+        uint32_t s_phase = 0, done = 0;  // steps of this tile, units of this tile
+        for (int r = 0;; r++) {
+            PromptUnit u;
+            bool got = fetch(r, u);
+            got = __all_sync(kFull, got);
+            __syncwarp();
+            if (lane == 0 && got) mbar_arrive(&sm.unit_free[r & 1]);
+            if (!got) {
+                ok = false;
+                break;
+            }
+            if (u.n < 0) break;
+            const Span sp(u, tt);
+            if (t >= sp.active) continue;
+            const int nst = sp.steps[t], tok_t = u.tok0 + t * tt;
+            const int pos = row < G * tt ? tok_t + row / G : -1;
+            float m_used = -INFINITY;
+            uint64_t l2 = pk2(0.0f, 0.0f);
+            for (int i = 0; i < nst; i++) {
+                ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[t], s_phase & 1u));
+                s_phase++;
+                if (!ok) break;
+                tc_fence_after();
+                float s[128];
+                {
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; c++) tmem_ld32_async(tm + 32 * c, x[c]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < 4; c++)
+#pragma unroll
+                        for (int e = 0; e < 32; e++) s[32 * c + e] = __uint_as_float(x[c][e]);
+                }
+                if (neg) {
+#pragma unroll
+                    for (int e = 0; e < 128; e++) s[e] = -s[e];
+                }
+                if (i * kKeys + kKeys - 1 > tok_t) {
+                    const int last = pos - i * kKeys;  // keys after it are masked
+#pragma unroll
+                    for (int e = 0; e < 128; e++)
+                        if (e > last) s[e] = -INFINITY;
+                }
+                float m8[8];
+#pragma unroll
+                for (int x = 0; x < 8; x++) {
+                    const float *v = s + 16 * x;
+                    m8[x] = max3(v[0], v[1], v[2]);
+#pragma unroll
+                    for (int e = 3; e < 15; e += 2) m8[x] = max3(m8[x], v[e], v[e + 1]);
+                    m8[x] = fmaxf(m8[x], v[15]);
+                }
+                const float raw = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+                const float mx = raw == -INFINITY ? -INFINITY : raw * sabs;
+                float factor = 1.0f;
+                if (i == 0) {
+                    m_used = mx;
+                } else if (mx > m_used + kLazy) {
+                    factor = ex2_approx(m_used - mx);
+                    m_used = mx;
+                }
+                // O holds the PV of the step before (complete before this S): rescale where a maximum moved
+                if (__any_sync(kFull, factor != 1.0f)) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {
+                        uint32_t x[32];
+                        tmem_ld32_async(tm + 128 + 32 * c, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; e++) x[e] = __float_as_uint(__uint_as_float(x[e]) * factor);
+                        tmem_st32(tm + 128 + 32 * c, x);
+                    }
+                    l2 = mul2(l2, pk2(factor, factor));
+                }
+                // a row without a key in range (past its sequence): every score is -inf and P is 0
+                const float off = m_used == -INFINITY ? 0.0f : -m_used;
+                const uint64_t sc2 = pk2(sabs, sabs), off2 = pk2(off, off);
+                uint64_t sum2[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
+#pragma unroll
+                for (int hh = 0; hh < 2; hh++) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; e++) {
+                        float x0, x1;
+                        upk2(fma2(pk2(s[64 * hh + 2 * e], s[64 * hh + 2 * e + 1]), sc2, off2), x0, x1);
+                        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                        sum2[e & 1] = add2(sum2[e & 1], pk2(p0, p1));
+                        w[e] = E::pack(p0, p1);
+                    }
+                    tmem_st32(tm + 32 * hh, w);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(hh == 0 ? &sm.p_half[t] : &sm.p_full[t]);
+                }
+                l2 = add2(l2, add2(sum2[0], sum2[1]));
+            }
+            if (!ok) break;
+            // the epilogue has read the unit before's ml
+            if (done > 0) ok = __all_sync(kFull, mbar_wait_bounded(&sm.o_free[t], (done - 1) & 1u));
+            if (!ok) break;
+            float la, lb;
+            upk2(l2, la, lb);
+            sm.ml[t][row] = make_float2(m_used, la + lb);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.ml_full[t]);
+            done++;
+        }
+    } else if (warp < 12) {
+        // ---- V of the mixed steps, then the epilogue ----
+        regs_dec<kRegsEpilogue>();
+        const int w = tid - 256, row = w;
+        const uint32_t lane_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        Ring ring;
+        uint32_t raw_phase = 0;  // bit s: parity of stage s's next mixed V
+        uint32_t done[kUnitTiles] = {0, 0};
+        for (int r = 0;; r++) {
+            PromptUnit u;
+            if (ok) ok = __all_sync(kFull, fetch(r, u));
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(&sm.unit_free[r & 1]);
+            // a warp whose wait ran out meets the others here, so that all four leave together
+            if (epilogue_any(!ok)) {
+                ok = false;
+                break;
+            }
+            if (u.n < 0) break;
+            const Span sp(u, tt);
+            bool wild = false;
+            for (int i = 0; i < sp.total && ok; i++) {
+                ring.next();
+                if (i >= sp.mixed) {
+                    ok = __all_sync(kFull, mbar_wait_bounded(&sm.kv_raw[ring.stage], raw_phase >> ring.stage & 1u));
+                    if (!ok) break;
+                    raw_phase ^= 1u << ring.stage;
+                    uint8_t *v = sm.kv[ring.stage];
+                    const int left = u.n - i * kKeys;  // keys of the step inside the sequence
+#pragma unroll 4
+                    for (int e = w; e < kTileBytes / 16; e += 128) {
+                        uint4 x = reinterpret_cast<const uint4 *>(v)[e];
+                        if ((e & 1023) >> 3 >= left) {  // (8 pieces a key in each half of the elements)
+                            reinterpret_cast<uint4 *>(v)[e] = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (E::wild(x.x) | E::wild(x.y) | E::wild(x.z) | E::wild(x.w)) {
+                            wild = true;
+                            uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int c = 0; c < 4; c++) {
+                                const uint32_t m = E::wild(y[c]);
+                                y[c] &= ~((m & 0x8000u ? 0xFFFFu : 0u) | (m & 0x80000000u ? 0xFFFF0000u : 0u));
+                            }
+                            reinterpret_cast<uint4 *>(v)[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.kv_clean[ring.stage]);
+                }
+                ring.next();  // V
+            }
+            wild = epilogue_any(wild);
+            for (int t = 0; t < sp.active && ok; t++) {
+                ok = __all_sync(kFull, mbar_wait_bounded(&sm.ml_full[t], done[t] & 1u) &&
+                                           mbar_wait_bounded(&sm.o_full[t], done[t] & 1u));
+                if (!ok) break;
+                done[t]++;
+                tc_fence_after();
+                const float2 ml = sm.ml[t][row];
+                const float inv = 1.0f / ml.y;
+                const int tok = u.tok0 + t * tt + row / G, hq = u.h * G + row % G;
+                const bool live = row < G * tt && tok < u.n;
+                uint32_t o[64];
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    uint32_t x[32];
+                    tmem_ld32_async(lane_tm + 256 * t + 128 + 32 * c, x);
+                    tmem_ld_wait();
+                    if (wild && live) {
+                        // values that are not finite, of the keys this row sees in the mixed steps
+                        for (int j = sp.mixed * kKeys; j <= tok; j++) {
+                            const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + 32 * c;
+#pragma unroll
+                            for (int e = 0; e < 32; e++) {
+                                const float y = E::value(vr[e]);
+                                if (!(fabsf(y) < INFINITY)) x[e] = __float_as_uint(__uint_as_float(x[e]) + y);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        o[16 * c + e] = E::pack(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.o_free[t]);
+                if (!live) continue;
+                const int64_t at = (int64_t)(u.c0 + tok) * p.num_q_heads + hq;
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * kHeadDim);
+#pragma unroll
+                for (int c = 0; c < 16; c++) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                if (p.lse) p.lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
+            }
+        }
+    } else {
+        regs_dec<kRegsIssue>();
+        if (warp == 12 && lane == 0) {
+            // ---- the MMA thread ----
+            const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.q[0])) >> 32);
+            const uint32_t hi_v = (uint32_t)(umma_desc_mn(smem_addr(sm.kv[0]), kKeys * 128, 1024) >> 32);
+            const uint32_t q_lo = (uint32_t)umma_desc(smem_addr(sm.q[0]));
+            const uint32_t k_lo = (uint32_t)umma_desc(smem_addr(sm.kv[0]));
+            const uint32_t v_lo = (uint32_t)umma_desc_mn(smem_addr(sm.kv[0]), kKeys * 128, 1024);
+            constexpr uint32_t kStep = kTileBytes >> 4;
+            Ring ring;                            // the K of the step whose S is issued next
+            uint32_t p_phase[kUnitTiles] = {0, 0}, uses[kUnitTiles] = {0, 0};
+            uint32_t full_phase = 0, clean_phase = 0;  // bit s: parity of stage s's next kv_full, kv_clean
+            auto wait_full = [&](uint32_t stage) {
+                const uint32_t parity = full_phase >> stage & 1u;
+                full_phase ^= 1u << stage;
+                return mbar_wait_bounded(&sm.kv_full[stage], parity);
+            };
+            auto issue_s = [&](int t, uint32_t stage) {
+                const uint32_t a = q_lo + t * kStep, b = k_lo + stage * kStep;
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++) {
+                    const uint32_t d = (uint32_t)(((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) >> 4);
+                    umma_f16_ss(tmem + 256 * t, a + d, hi, b + d, hi, E::kIdescS, ks > 0 ? 1u : 0u);
+                }
+                umma_commit(&sm.s_full[t]);
+            };
+            auto issue_pv = [&](int t, uint32_t stage, int half, bool first) {
+                const uint32_t d = tmem + 256 * t, b = v_lo + stage * kStep;
+#pragma unroll
+                for (int x = 0; x < 4; x++) {
+                    const int ks = 4 * half + x;
+                    umma_f16_ts(d + 128, d + 8 * ks, b + (uint32_t)((ks * 16 * 128) >> 4), hi_v, E::kIdescO,
+                                (first && ks == 0) ? 0u : 1u);
+                }
+            };
+            for (int r = 0; ok; r++) {
+                PromptUnit u;
+                if (!fetch(r, u)) break;
+                mbar_arrive(&sm.unit_free[r & 1]);
+                if (u.n < 0) break;
+                const Span sp(u, tt);
+                const int end = sp.active - 1;  // the tile with the most steps
+                ok = wait_full(ring.stage);
+                for (int t = 0; t < sp.active && ok; t++) {
+                    ok = mbar_wait_bounded(&sm.q_full[t], uses[t] & 1u);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_s(t, ring.stage);
+                    if (sp.steps[t] == 1) umma_commit(&sm.q_free[t]);
+                }
+                if (!ok) break;
+                umma_commit(&sm.kv_free[ring.stage]);
+                ring.next();
+                for (int i = 0; i < sp.total && ok; i++) {
+                    const Ring v = ring;
+                    ring.next();
+                    bool v_seen = false, k_seen = false;
+                    for (int t = 0; t < sp.active && ok; t++) {
+                        if (i >= sp.steps[t]) continue;
+                        ok = mbar_wait_bounded(&sm.p_half[t], p_phase[t]);
+                        if (ok && i == 0 && uses[t] > 0)
+                            ok = mbar_wait_bounded(&sm.o_free[t], (uses[t] - 1) & 1u);
+                        if (ok && !v_seen) {
+                            if (i >= sp.mixed) {
+                                ok = mbar_wait_bounded(&sm.kv_clean[v.stage], clean_phase >> v.stage & 1u);
+                                clean_phase ^= 1u << v.stage;
+                            } else {
+                                ok = wait_full(v.stage);
+                            }
+                            v_seen = true;
+                        }
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(t, v.stage, 0, i == 0);
+                        ok = mbar_wait_bounded(&sm.p_full[t], p_phase[t]);
+                        p_phase[t] ^= 1u;
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(t, v.stage, 1, false);
+                        if (i + 1 == sp.steps[t]) {
+                            umma_commit(&sm.o_full[t]);
+                            uses[t]++;
+                        }
+                        if (t == end) umma_commit(&sm.kv_free[v.stage]);
+                        if (i + 1 < sp.steps[t]) {
+                            // over P of this step: the tensor pipe runs one thread's MMAs in order
+                            if (!k_seen) ok = wait_full(ring.stage);
+                            k_seen = true;
+                            if (!ok) break;
+                            tc_fence_after();
+                            issue_s(t, ring.stage);
+                            if (i + 2 == sp.steps[t]) umma_commit(&sm.q_free[t]);
+                            if (t == end) umma_commit(&sm.kv_free[ring.stage]);
+                        }
+                    }
+                    if (i + 1 < sp.total) ring.next();
+                }
+            }
+            umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
+            if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
+        } else if (warp == 13) {
+            // ---- units and copies ----
+            const int H = p.num_heads, ut = kUnitTiles * tt;
+            // a sequence's length, 0 where its bounds are broken
+            auto length = [&](int b) {
+                const int c0 = p.cu[b], n = p.cu[b + 1] - c0;
+                const bool good = n >= 0 && n <= p.max_n && c0 >= 0 && (int64_t)c0 + n <= p.total;
+                if (!good && blockIdx.x == 0) set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
+                return good ? n : 0;
+            };
+            const bool few = p.num_seqs <= 32;  // lengths stay in registers
+            const int mine = few && lane < p.num_seqs ? length(lane) : 0;
+            // sequences (of 32 from b0 on) with a unit number x, as a mask
+            auto longer = [&](int b0, int64_t x) {
+                const int n = few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0;
+                return __ballot_sync(kFull, n > x * ut);
+            };
+            auto level = [&](int64_t x) {
+                int c = 0;
+                for (int b0 = 0; b0 < p.num_seqs; b0 += 32) c += __popc(longer(b0, x));
+                return c;
+            };
+            int64_t x = (p.max_n + ut - 1) / ut - 1, base = 0;  // units before level x
+            int count = level(x);                                // sequences on level x
+            Ring ring;
+            uint32_t used = 0;  // stages filled so far, up to kStages
+            // bit s: parity of stage s's next kv_full, kv_raw; whether its last fill was a mixed V
+            uint32_t full_phase = 0, raw_phase = 0, last_raw = 0;
+            uint32_t uses[kUnitTiles] = {0, 0};
+            for (int r = 0;; r++) {
+                const int64_t id = (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                while (x >= 0 && id >= base + (int64_t)count * H) {
+                    base += (int64_t)count * H;
+                    if (--x >= 0) count = level(x);
+                }
+                PromptUnit u = {0, -1, 0, 0};
+                if (x >= 0) {
+                    const int64_t rank = id - base;
+                    int k = (int)(rank / H);  // the k-th sequence of the level
+                    u.h = (int)(rank % H);
+                    for (int b0 = 0;; b0 += 32) {
+                        uint32_t m = longer(b0, x);
+                        const int c = __popc(m);
+                        if (k >= c) {
+                            k -= c;
+                            continue;
+                        }
+                        const int b = b0 + (int)__fns(m, 0, k + 1);
+                        u.c0 = p.cu[b];
+                        u.n = p.cu[b + 1] - u.c0;
+                        break;
+                    }
+                    u.tok0 = (int)(x * ut);
+                }
+                ok = __all_sync(kFull, r < 2 || mbar_wait_bounded(&sm.unit_free[r & 1], (uint32_t)((r >> 1) - 1) & 1u));
+                if (!ok) break;
+                if (lane == 0) {
+                    sm.unit[r & 1] = u;
+                    mbar_arrive(&sm.unit_full[r & 1]);
+                }
+                if (u.n < 0) break;
+                if (lane == 0) {
+                    const Span sp(u, tt);
+                    auto stage = [&](const CUtensorMap *map, int key, bool raw) {
+                        if (used >= kStages) ok = mbar_wait_bounded(&sm.kv_free[ring.stage], ring.phase ^ 1u);
+                        if (!ok) return;
+                        const uint32_t bit = 1u << ring.stage;
+                        uint64_t *bar = raw ? &sm.kv_raw[ring.stage] : &sm.kv_full[ring.stage];
+                        if (raw)
+                            raw_phase ^= bit;
+                        else
+                            full_phase ^= bit;
+                        last_raw = raw ? last_raw | bit : last_raw & ~bit;
+                        uint8_t *dst = sm.kv[ring.stage];
+                        mbar_arrive_expect_tx(bar, kTileBytes);
+                        tma_load_3d(dst, map, 0, u.h, u.c0 + key, bar);
+                        tma_load_3d(dst + kTileBytes / 2, map, 64, u.h, u.c0 + key, bar);
+                        if (used < kStages) used++;
+                        ring.next();
+                    };
+                    for (int i = 0; i < sp.total && ok; i++) {
+                        stage(&map_k, i * kKeys, false);
+                        for (int t = 0; i == 0 && t < sp.active && ok; t++) {
+                            if (uses[t] > 0) ok = mbar_wait_bounded(&sm.q_free[t], (uses[t] - 1) & 1u);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * G * tt);
+                            const int tok = u.c0 + u.tok0 + t * tt;
+                            tma_load_3d(sm.q[t], &map_q, 0, u.h * G, tok, &sm.q_full[t]);
+                            tma_load_3d(sm.q[t] + kTileBytes / 2, &map_q, 64, u.h * G, tok, &sm.q_full[t]);
+                            uses[t]++;
+                        }
+                        if (ok) stage(&map_v, i * kKeys, i >= sp.mixed);
+                    }
+                }
+                ok = __all_sync(kFull, ok);
+                if (!ok) break;
+            }
+            if (lane == 0) {  // no copy in flight when the CTA ends
+                for (uint32_t s = 0; s < used; s++) {
+                    const bool raw = last_raw >> s & 1u;
+                    const uint32_t next = (raw ? raw_phase : full_phase) >> s & 1u;
+                    if (!mbar_wait_bounded(raw ? &sm.kv_raw[s] : &sm.kv_full[s], next ^ 1u)) ok = false;
+                }
+                for (int t = 0; t < kUnitTiles; t++)
+                    if (uses[t] > 0 && !mbar_wait_bounded(&sm.q_full[t], (uses[t] - 1) & 1u)) ok = false;
+            }
+        }
+    }
+    __syncwarp();
+    if (!ok) set_flag(p.status, KVQ_FLAG_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPromptTmem));
+}
+
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled()
+{
+    static const EncodeTiled fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// rows of [heads][128] 16-bit elements, `stride` elements apart: boxes of 64 elements x `box_heads` x `box_rows`,
+// 128-byte swizzled (rows past the tensor read as zero)
+bool make_map(CUtensorMap *m, bool bf, const uint16_t *x, int64_t rows, int heads, int64_t stride, int box_heads,
+              int box_rows)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {kHeadDim * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, one[3] = {1, 1, 1};
+    return encode_tiled()(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                          const_cast<uint16_t *>(x), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BF>
+cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                               int64_t k_stride, int num_sms, cudaStream_t s)
+{
+    CUtensorMap mq, mk, mv;
+    if (!encode_tiled()) return cudaErrorNotSupported;
+    if (!make_map(&mq, BF, q, p.total, p.num_q_heads, q_stride, p.group, p.tile_tokens) ||
+        !make_map(&mk, BF, k, p.total, p.num_heads, k_stride, 1, kKeys) ||
+        !make_map(&mv, BF, p.v, p.total, p.num_heads, p.v_stride, 1, kKeys))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(PromptSmem));
+    if (e != cudaSuccess) return e;
+    // at most one CTA per SM, and no more than there can be units
+    const int64_t ut = kUnitTiles * p.tile_tokens;
+    const int64_t by_max = (int64_t)p.num_seqs * ((p.max_n + ut - 1) / ut), by_total = p.total / ut + p.num_seqs;
+    const int64_t units = (by_max < by_total ? by_max : by_total) * p.num_heads;
+    const int grid = units < num_sms ? (int)units : num_sms;
+    return launch_plain(prompt_attn_kernel<BF>, dim3((unsigned)grid), dim3(kPromptThreads), sizeof(PromptSmem), s, p,
+                        mq, mk, mv);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt(int dtype, const PromptParams &p, const uint16_t *q, int64_t q_stride, const uint16_t *k,
+                          int64_t k_stride, int num_sms, cudaStream_t s)
+{
+    return dtype == KVQ_BF16 ? launch_prompt_type<true>(p, q, q_stride, k, k_stride, num_sms, s)
+                             : launch_prompt_type<false>(p, q, q_stride, k, k_stride, num_sms, s);
+}
+
+}  // namespace kvq

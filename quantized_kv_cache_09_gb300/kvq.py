@@ -20,6 +20,8 @@ from . import build as _build
 KVQ_INT4_B64 = 0
 KVQ_INT8_PAGE = 1
 KVQ_FP8_E4M3 = 2
+KVQ_FP16 = 0
+KVQ_BF16 = 1
 HEAD_DIM = 128
 PAGE_TOKENS = 64
 
@@ -38,6 +40,7 @@ STATUS_NAMES = {0: "KVQ_OK", 1: "KVQ_ERR_INVALID_ARG", 2: "KVQ_ERR_UNSUPPORTED",
 EXPORTS = ("kvq_quantize", "kvq_append", "kvq_decode_workspace_bytes", "kvq_decode_attention",
            "kvq_decode_workspace_bytes_gqa", "kvq_decode_attention_gqa",
            "kvq_decode_attention_noalloc", "kvq_prefill_workspace_bytes", "kvq_prefill_attention",
+           "kvq_prompt_attention", "kvq_page_weights_workspace_bytes", "kvq_page_weights", "kvq_evict_pages",
            "kvq_step_graph_create", "kvq_step_graph_update",
            "kvq_step_graph_launch", "kvq_step_graph_destroy", "kvq_get_device_status", "kvq_status_string",
            "kvq_version")
@@ -127,6 +130,16 @@ def lib():
         L.kvq_prefill_attention.argtypes = [cp, vp, i32, vp, i64, i32, vp, i32, vp, i32, ctypes.c_float, vp, vp, sz,
                                             vp]
         L.kvq_prefill_attention.restype = ctypes.c_int
+        L.kvq_prompt_attention.argtypes = [ctypes.c_int, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, i64, i32, i32,
+                                           ctypes.c_float, vp, vp, vp, vp]
+        L.kvq_prompt_attention.restype = ctypes.c_int
+        L.kvq_page_weights_workspace_bytes.argtypes = [i64, i32, i32]
+        L.kvq_page_weights_workspace_bytes.restype = sz
+        L.kvq_page_weights.argtypes = [cp, vp, i32, vp, i64, i32, vp, i32, vp, i32, ctypes.c_float, ctypes.c_float,
+                                       vp, vp, vp, sz, vp]
+        L.kvq_page_weights.restype = ctypes.c_int
+        L.kvq_evict_pages.argtypes = [vp, i32, vp, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.kvq_evict_pages.restype = ctypes.c_int
         ap = ctypes.POINTER(kvq_step_args)
         L.kvq_step_graph_create.argtypes = [cp, ap, i32, ctypes.POINTER(vp)]
         L.kvq_step_graph_create.restype = ctypes.c_int
@@ -168,6 +181,11 @@ def _check(rc, what):
 def _cuda(t, dtype, name):
     if not (t.is_cuda and t.is_contiguous() and t.dtype == dtype):
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+
+
+def _one_device(*tensors):
+    if len({t.device for t in tensors if t is not None}) > 1:
+        raise ValueError("the tensors are on different devices")
 
 
 def kvq_status_string(status):
@@ -318,6 +336,117 @@ def kvq_prefill_attention(cache, q, cu_seqlens_q, max_q_per_seq, block_table, se
                                        _stream(stream, q.device)), "kvq_prefill_attention")
 
 
+def _rows(t, dtype, name):
+    """The row stride of a CUDA tensor [rows][heads][128] whose rows have no gaps of their own."""
+    if not (t.is_cuda and t.dim() == 3 and t.dtype == dtype and t.shape[2] == HEAD_DIM):
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor [rows][heads][{HEAD_DIM}]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM):
+        raise ValueError(f"{name}: the heads of a row must lie side by side")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+
+
+@_nvtx
+def kvq_prompt_attention(q, k, v, cu_seqlens, max_tokens_per_seq, softmax_scale, out, lse=None, status=None,
+                         stream=None):
+    """out [total][Hq][128] = causal attention of whole prompts over their own
+    rows: q [total][Hq][128], k and v [total][H][128] in fp16 or bf16, sequence
+    b in rows cu[b] .. cu[b+1]-1, query head i reading head i // (Hq / H).  q, k
+    and v may be views with gaps between rows (slices of one fused projection).
+    lse (optional) fp32 [total][Hq]: ln of the softmax's denominator.  status
+    (optional) int32[1]: KVQ_FLAG_* bits, e.g. the cache's status word."""
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be a CUDA float16 or bfloat16 tensor")
+    strides = [_rows(t, q.dtype, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    _cuda(out, q.dtype, "out")
+    _cuda(cu_seqlens, torch.int32, "cu_seqlens")
+    if lse is not None:
+        _cuda(lse, torch.float32, "lse")
+    if status is not None:
+        _cuda(status, torch.int32, "status")
+    T, Hq = q.shape[:2]
+    if (out.shape != q.shape or k.shape != v.shape or k.shape[0] != T or cu_seqlens.dim() != 1 or
+            cu_seqlens.numel() < 1 or (lse is not None and tuple(lse.shape) != (T, Hq)) or
+            (status is not None and status.numel() < 1)):
+        raise ValueError("q/k/v/out/lse/cu_seqlens shapes disagree")
+    _one_device(q, k, v, out, cu_seqlens, lse, status)
+    with torch.cuda.device(q.device):
+        _check(lib().kvq_prompt_attention(KVQ_BF16 if q.dtype == torch.bfloat16 else KVQ_FP16, _ptr(q), strides[0],
+                                          _ptr(k), strides[1], _ptr(v), strides[2], Hq, k.shape[1], HEAD_DIM,
+                                          _ptr(cu_seqlens), T, int(max_tokens_per_seq), cu_seqlens.numel() - 1,
+                                          float(softmax_scale), _ptr(out), _ptr(lse), _ptr(status),
+                                          _stream(stream, q.device)), "kvq_prompt_attention")
+
+
+def kvq_page_weights_workspace_bytes(total_q, num_q_heads, max_blocks_per_seq):
+    return int(lib().kvq_page_weights_workspace_bytes(int(total_q), int(num_q_heads), int(max_blocks_per_seq)))
+
+
+def page_weights_workspace(total_q, num_q_heads, max_blocks_per_seq, device="cuda"):
+    """A workspace for kvq_page_weights (reusable by calls of at most these sizes, one call at a time)."""
+    n = kvq_page_weights_workspace_bytes(total_q, num_q_heads, max_blocks_per_seq)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+@_nvtx
+def kvq_page_weights(cache, q, cu_seqlens_q, max_q_per_seq, block_table, seq_lens, softmax_scale, decay, weights_in,
+                     weights_out, workspace, stream=None):
+    """weights_out fp32 [B][max_blocks] = decay * weights_in (None: 0) + the
+    softmax weight that each page receives from the newest queries q fp16
+    [total][Hq][128] of its sequence (sequence b's are rows cu[b] .. cu[b+1]-1,
+    its last tokens; one row each in a decode step), summed over heads and
+    queries.  weights_out may be weights_in."""
+    _cuda(q, torch.float16, "q")
+    for t, n in ((cu_seqlens_q, "cu_seqlens_q"), (block_table, "block_table"), (seq_lens, "seq_lens")):
+        _cuda(t, torch.int32, n)
+    _cuda(weights_out, torch.float32, "weights_out")
+    if weights_in is not None:
+        _cuda(weights_in, torch.float32, "weights_in")
+    _cuda(workspace, torch.uint8, "workspace")
+    B = seq_lens.numel()
+    if (q.dim() != 3 or q.shape[2] != HEAD_DIM or cu_seqlens_q.numel() != B + 1 or block_table.dim() != 2 or
+            block_table.shape[0] != B or weights_out.shape != block_table.shape or
+            (weights_in is not None and weights_in.shape != block_table.shape)):
+        raise ValueError("q/cu_seqlens_q/seq_lens/block_table/weights shapes disagree")
+    _one_device(q, cu_seqlens_q, block_table, seq_lens, weights_in, weights_out, workspace)
+    with torch.cuda.device(q.device):
+        _check(lib().kvq_page_weights(ctypes.byref(cache.struct), _ptr(q), q.shape[1], _ptr(cu_seqlens_q), q.shape[0],
+                                      int(max_q_per_seq), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
+                                      float(softmax_scale), float(decay), _ptr(weights_in), _ptr(weights_out),
+                                      _ptr(workspace), workspace.numel(), _stream(stream, q.device)),
+               "kvq_page_weights")
+
+
+@_nvtx
+def kvq_evict_pages(block_table, seq_lens, weights, keep_blocks, sink_blocks, recent_blocks, table_out, seq_lens_out,
+                    weights_out, num_evicted, status=None, stream=None):
+    """Let the pages of least weight leave each row of block_table int32
+    [B][max_blocks] until keep_blocks[b] are left; the first sink_blocks and the
+    last max(recent_blocks, 1) pages always stay.  table_out: kept pages, then
+    the entries past the length, then the num_evicted[b] evicted pages;
+    seq_lens_out and weights_out follow.  An output may be its own input."""
+    for t, n in ((block_table, "block_table"), (seq_lens, "seq_lens"), (keep_blocks, "keep_blocks"),
+                 (table_out, "table_out"), (seq_lens_out, "seq_lens_out"), (num_evicted, "num_evicted")):
+        _cuda(t, torch.int32, n)
+    _cuda(weights, torch.float32, "weights")
+    _cuda(weights_out, torch.float32, "weights_out")
+    if status is not None:
+        _cuda(status, torch.int32, "status")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [num_seqs][max_blocks_per_seq]")
+    B, mb = block_table.shape
+    if (table_out.shape != block_table.shape or weights.shape != block_table.shape or
+            weights_out.shape != block_table.shape or
+            any(t.numel() != B for t in (seq_lens, keep_blocks, seq_lens_out, num_evicted)) or
+            (status is not None and status.numel() < 1)):
+        raise ValueError("block_table/seq_lens/weights/keep_blocks shapes disagree")
+    _one_device(block_table, seq_lens, weights, keep_blocks, table_out, seq_lens_out, weights_out, num_evicted, status)
+    with torch.cuda.device(block_table.device):
+        _check(lib().kvq_evict_pages(_ptr(block_table), mb, _ptr(seq_lens), _ptr(weights), B, _ptr(keep_blocks),
+                                     int(sink_blocks), int(recent_blocks), _ptr(table_out), _ptr(seq_lens_out),
+                                     _ptr(weights_out), _ptr(num_evicted), _ptr(status),
+                                     _stream(stream, block_table.device)), "kvq_evict_pages")
+
+
 class StepGraph:
     """kvq_step_graph_*: a sequence of decode steps -- each appends one chunk of
     new tokens per sequence, then runs decode attention over the grown
@@ -428,6 +557,43 @@ class PagedKVCache:
                                 None if self.v_tail is None else self.v_tail.data_ptr(),
                                 self.status.data_ptr())
 
+    @classmethod
+    def over(cls, fmt, k_codes, v_codes, k_scales, v_scales, k_tail=None, v_tail=None, status=None):
+        """The descriptor of a cache in buffers that exist already: codes uint8
+        [num_pages][heads][64][64 or 128], scales fp32 [num_pages][heads], tails
+        (both or neither) fp16 [max_seqs][heads][64][128], status int32[1]
+        (None: a new word)."""
+        self = cls.__new__(cls)
+        rb = HEAD_DIM // 2 if int(fmt) == KVQ_INT4_B64 else HEAD_DIM
+        for t, n in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _cuda(t, torch.uint8, n)
+        for t, n in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _cuda(t, torch.float32, n)
+        shape = tuple(k_codes.shape)
+        if (len(shape) != 4 or shape[2:] != (PAGE_TOKENS, rb) or v_codes.shape != k_codes.shape or
+                tuple(k_scales.shape) != shape[:2] or v_scales.shape != k_scales.shape):
+            raise ValueError("codes must be [num_pages][heads][64][row bytes] and scales [num_pages][heads]")
+        if (k_tail is None) != (v_tail is None):
+            raise ValueError("tails of K and V come together")
+        for t, n in ((k_tail, "k_tail"), (v_tail, "v_tail")):
+            if t is not None:
+                _cuda(t, torch.float16, n)
+                if t.dim() != 4 or tuple(t.shape[1:]) != (shape[1], PAGE_TOKENS, HEAD_DIM) or t.shape != k_tail.shape:
+                    raise ValueError(f"{n} must be [max_seqs][heads][64][128]")
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=k_codes.device)
+        _cuda(status, torch.int32, "status")
+        _one_device(k_codes, v_codes, k_scales, v_scales, k_tail, v_tail, status)
+        self.fmt, self.num_pages, self.num_heads, self.row_bytes = int(fmt), shape[0], shape[1], rb
+        self.max_seqs = 0 if k_tail is None else k_tail.shape[0]
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.k_tail, self.v_tail, self.status = k_tail, v_tail, status
+        self.struct = kvq_cache(self.fmt, self.num_heads, HEAD_DIM, PAGE_TOKENS, self.num_pages, self.max_seqs,
+                                k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                None if k_tail is None else k_tail.data_ptr(),
+                                None if v_tail is None else v_tail.data_ptr(), status.data_ptr())
+        return self
+
     def rows_from(self, b0):
         """A descriptor of the same cache whose tail rows start at sequence row b0,
         for an append call that covers sequences b0, b0+1, ... of a larger batch."""
@@ -454,4 +620,6 @@ class PagedKVCache:
 __all__ = ["KVQ_INT4_B64", "KVQ_INT8_PAGE", "KVQ_FP8_E4M3", "HEAD_DIM", "PAGE_TOKENS", "EXPORTS", "KvqError", "kvq_cache",
            "PagedKVCache", "lib", "library_path", "kvq_quantize", "kvq_append", "kvq_decode_workspace_bytes",
            "kvq_decode_attention", "kvq_decode_attention_noalloc", "kvq_get_device_status", "kvq_status_string",
-           "kvq_version", "StepGraph", "kvq_step_args", "kvq_prefill_attention"]
+           "kvq_version", "StepGraph", "kvq_step_args", "kvq_prefill_attention", "KVQ_FP16", "KVQ_BF16",
+           "kvq_prompt_attention", "kvq_page_weights", "kvq_page_weights_workspace_bytes", "page_weights_workspace",
+           "kvq_evict_pages"]
