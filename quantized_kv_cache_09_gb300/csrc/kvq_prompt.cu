@@ -26,7 +26,10 @@
 //             are not finite taken out (0 * inf would reach rows that do not see
 //             them; the epilogue adds them to the rows that do).  Then the
 //             epilogue: O / l, while the tensor cores are on the next unit.
-//   12        issues the MMAs (one thread): S = Q K^T, O += P V, M = N = 128.
+//   12, 14    one thread each issues the MMAs of a tile: S = Q K^T, O += P V,
+//             M = N = 128.  (An MMA holds its issuer until the tensor pipe takes it,
+//             and a wait between MMAs costs ~100 cycles: with one thread for both
+//             tiles the pipe was busy 49% of the time.)
 //   13        walks the unit list and issues the TMA copies: Q tiles and a ring
 //             of five 32 KB stages, K and V alternating.
 // While one tile's rows are in the softmax, the tensor cores work on the other.
@@ -35,6 +38,8 @@
 // keys) first, over sequences and cache heads, dealt to the CTAs forwards and
 // backwards in turn -- longest first without a counter to fetch from.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "kvq_around.h"
 #include "kvq_device.cuh"
@@ -49,6 +54,7 @@ constexpr int kTileRows = 128;
 constexpr int kUnitTiles = 2;
 constexpr int kKeys = 128;
 constexpr int kStages = 5;
+constexpr int kParts = 3;  // P is handed over as keys 0..63, 64..95, 96..127
 constexpr int kTileBytes = kTileRows * kHeadDim * 2;
 constexpr int kPromptThreads = 512;
 constexpr uint32_t kPromptTmem = 512;  // tile t: S / P at columns 256 t, O at 256 t + 128
@@ -56,9 +62,12 @@ constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 // a softmax scale of 0 scores 1e-38 * raw instead, so that a masked score stays -inf
 constexpr float kMinScale = 1.17549435e-38f;
-// registers per thread after the split: 2 * 176 + 104 + 56 = 4 * 128, the launch's
-constexpr int kRegsSoftmax = 176, kRegsEpilogue = 104, kRegsIssue = 56;
+// registers per thread after the split: 2 * 184 + 80 + 64 = 4 * 128, the launch's
+constexpr int kRegsSoftmax = 184, kRegsEpilogue = 80, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsIssue <= 4 * (65536 / kPromptThreads), "register split");
+
+template <int N>
+using Int = std::integral_constant<int, N>;
 
 // 16-bit element type: fp16 or bf16
 template <bool BF>
@@ -103,8 +112,8 @@ struct alignas(1024) PromptSmem {
     uint64_t kv_free[kStages];   // the MMAs that read the stage complete
     uint64_t q_full[kUnitTiles], q_free[kUnitTiles];
     uint64_t s_full[kUnitTiles];   // S of a step complete, and every MMA before it
-    uint64_t p_half[kUnitTiles];   // P of keys 0..63 in tensor memory, O rescaled
-    uint64_t p_full[kUnitTiles];   // P of keys 64..127
+    uint64_t p_full[kUnitTiles][kParts];  // a part of P in tensor memory (the first: O rescaled too)
+    uint64_t turn[kUnitTiles];     // the MMA thread of a tile may issue
     uint64_t o_full[kUnitTiles];   // a unit's last PV complete
     uint64_t o_free[kUnitTiles];   // O and ml read by the epilogue
     uint64_t ml_full[kUnitTiles];  // a unit's maxima and sums written
@@ -186,7 +195,7 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 
 }  // namespace
 
-template <bool BF>
+template <bool BF, bool NEG>
 __global__ void __launch_bounds__(kPromptThreads, 1)
     prompt_attn_kernel(PromptParams p, const __grid_constant__ CUtensorMap map_q,
                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(&sm.kv_full[s], 1);
-            mbar_init(&sm.kv_free[s], 1);
+            mbar_init(&sm.kv_free[s], 2);  // both MMA threads
             mbar_init(&sm.kv_raw[s], 1);
             mbar_init(&sm.kv_clean[s], 4);
         }
@@ -208,17 +217,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mbar_init(&sm.q_full[t], 1);
             mbar_init(&sm.q_free[t], 1);
             mbar_init(&sm.s_full[t], 1);
-            mbar_init(&sm.p_half[t], 4);
-            mbar_init(&sm.p_full[t], 4);
+            for (int x = 0; x < kParts; x++) mbar_init(&sm.p_full[t][x], 4);
+            mbar_init(&sm.turn[t], 1);
             mbar_init(&sm.o_full[t], 1);
             mbar_init(&sm.o_free[t], 4);
             mbar_init(&sm.ml_full[t], 4);
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(&sm.unit_full[s], 1);
-            mbar_init(&sm.unit_free[s], 13);  // 8 softmax warps, 4 epilogue warps, the MMA thread
+            mbar_init(&sm.unit_free[s], 14);  // 8 softmax warps, 4 epilogue warps, 2 MMA threads
         }
-        mbar_init(&sm.mma_done, 1);
+        mbar_init(&sm.mma_done, 2);
         mbar_init_fence();
     }
     if (warp == 12) {
@@ -245,7 +254,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         const int t = warp >> 2, row = tid & 127;
         const uint32_t tm = tmem + 256u * t + ((uint32_t)((warp & 3) * 32) << 16);
         const float sabs = fmaxf(fabsf(p.score_scale), kMinScale);
-        const bool neg = p.score_scale < 0.0f;
         uint32_t s_phase = 0, done = 0;  // steps of this tile, units of this tile
         for (int r = 0;; r++) {
             PromptUnit u;
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; e++) s[32 * c + e] = __uint_as_float(x[c][e]);
                 }
-                if (neg) {
+                if constexpr (NEG) {  // a negative softmax scale
 #pragma unroll
                     for (int e = 0; e < 128; e++) s[e] = -s[e];
                 }
@@ -325,23 +333,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const float off = m_used == -INFINITY ? 0.0f : -m_used;
                 const uint64_t sc2 = pk2(sabs, sabs), off2 = pk2(off, off);
                 uint64_t sum2[2] = {pk2(0.0f, 0.0f), pk2(0.0f, 0.0f)};
+                auto part = [&](auto first, auto count, uint64_t *bar) {  // pairs of keys
+                    constexpr int A = decltype(first)::value, N = decltype(count)::value;
+                    uint32_t w[N];
 #pragma unroll
-                for (int hh = 0; hh < 2; hh++) {
-                    uint32_t w[32];
-#pragma unroll
-                    for (int e = 0; e < 32; e++) {
+                    for (int e = 0; e < N; e++) {
                         float x0, x1;
-                        upk2(fma2(pk2(s[64 * hh + 2 * e], s[64 * hh + 2 * e + 1]), sc2, off2), x0, x1);
+                        upk2(fma2(pk2(s[2 * (A + e)], s[2 * (A + e) + 1]), sc2, off2), x0, x1);
                         const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                         sum2[e & 1] = add2(sum2[e & 1], pk2(p0, p1));
                         w[e] = E::pack(p0, p1);
                     }
-                    tmem_st32(tm + 32 * hh, w);
+                    if constexpr (N == 32)
+                        tmem_st32(tm + A, w);
+                    else
+                        tmem_st16(tm + A, w);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(hh == 0 ? &sm.p_half[t] : &sm.p_full[t]);
-                }
+                    if (lane == 0) mbar_arrive(bar);
+                };
+                part(Int<0>(), Int<32>(), &sm.p_full[t][0]);
+                part(Int<32>(), Int<16>(), &sm.p_full[t][1]);
+                part(Int<48>(), Int<16>(), &sm.p_full[t][2]);
                 l2 = add2(l2, add2(sum2[0], sum2[1]));
             }
             if (!ok) break;
@@ -417,73 +431,73 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const float inv = 1.0f / ml.y;
                 const int tok = u.tok0 + t * tt + row / G, hq = u.h * G + row % G;
                 const bool live = row < G * tt && tok < u.n;
-                uint32_t o[64];
+                const int64_t at = (int64_t)(u.c0 + tok) * p.num_q_heads + hq;
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t x[32];
-                    tmem_ld32_async(lane_tm + 256 * t + 128 + 32 * c, x);
-                    tmem_ld_wait();
-                    if (wild && live) {
-                        // values that are not finite, of the keys this row sees in the mixed steps
-                        for (int j = sp.mixed * kKeys; j <= tok; j++) {
-                            const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + 32 * c;
+                for (int half = 0; half < 2; half++) {
+                    uint32_t o[32];
 #pragma unroll
-                            for (int e = 0; e < 32; e++) {
-                                const float y = E::value(vr[e]);
-                                if (!(fabsf(y) < INFINITY)) x[e] = __float_as_uint(__uint_as_float(x[e]) + y);
+                    for (int c = 0; c < 2; c++) {
+                        const int col = 64 * half + 32 * c;
+                        uint32_t x[32];
+                        tmem_ld32_async(lane_tm + 256 * t + 128 + col, x);
+                        tmem_ld_wait();
+                        if (wild && live) {
+                            // values that are not finite, of the keys this row sees in the mixed steps
+                            for (int j = sp.mixed * kKeys; j <= tok; j++) {
+                                const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + col;
+#pragma unroll
+                                for (int e = 0; e < 32; e++) {
+                                    const float y = E::value(vr[e]);
+                                    if (!(fabsf(y) < INFINITY)) x[e] = __float_as_uint(__uint_as_float(x[e]) + y);
+                                }
                             }
                         }
+#pragma unroll
+                        for (int e = 0; e < 16; e++)
+                            o[16 * c + e] =
+                                E::pack(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
                     }
+                    if (half == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm.o_free[t]);
+                    }
+                    if (live) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * kHeadDim + 64 * half);
 #pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        o[16 * c + e] = E::pack(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+                        for (int c = 0; c < 8; c++)
+                            dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.o_free[t]);
                 if (!live) continue;
-                const int64_t at = (int64_t)(u.c0 + tok) * p.num_q_heads + hq;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * kHeadDim);
-#pragma unroll
-                for (int c = 0; c < 16; c++) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 if (p.lse) p.lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
             }
         }
     } else {
         regs_dec<kRegsIssue>();
-        if (warp == 12 && lane == 0) {
-            // ---- the MMA thread ----
+        if (warp != 13 && warp - 12 <= 2 && lane == 0) {
+            // ---- the MMA thread of tile t (warps 12 and 14) ----
+            const int t = (warp - 12) >> 1;
+            const uint32_t tm = tmem + 256 * t;
             const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.q[0])) >> 32);
             const uint32_t hi_v = (uint32_t)(umma_desc_mn(smem_addr(sm.kv[0]), kKeys * 128, 1024) >> 32);
-            const uint32_t q_lo = (uint32_t)umma_desc(smem_addr(sm.q[0]));
+            const uint32_t q_lo = (uint32_t)umma_desc(smem_addr(sm.q[t]));
             const uint32_t k_lo = (uint32_t)umma_desc(smem_addr(sm.kv[0]));
             const uint32_t v_lo = (uint32_t)umma_desc_mn(smem_addr(sm.kv[0]), kKeys * 128, 1024);
             constexpr uint32_t kStep = kTileBytes >> 4;
-            Ring ring;                            // the K of the step whose S is issued next
-            uint32_t p_phase[kUnitTiles] = {0, 0}, uses[kUnitTiles] = {0, 0};
+            Ring ring;                                 // the stage to read next, K and V alternating
+            uint32_t p_phase = 0, turn_phase = 0, uses = 0;
             uint32_t full_phase = 0, clean_phase = 0;  // bit s: parity of stage s's next kv_full, kv_clean
+            if (t == 0) mbar_arrive(&sm.turn[0]);  // tile 0 begins
             auto wait_full = [&](uint32_t stage) {
                 const uint32_t parity = full_phase >> stage & 1u;
                 full_phase ^= 1u << stage;
                 return mbar_wait_bounded(&sm.kv_full[stage], parity);
             };
-            auto issue_s = [&](int t, uint32_t stage) {
-                const uint32_t a = q_lo + t * kStep, b = k_lo + stage * kStep;
-#pragma unroll
-                for (int ks = 0; ks < 8; ks++) {
-                    const uint32_t d = (uint32_t)(((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) >> 4);
-                    umma_f16_ss(tmem + 256 * t, a + d, hi, b + d, hi, E::kIdescS, ks > 0 ? 1u : 0u);
-                }
-                umma_commit(&sm.s_full[t]);
-            };
-            auto issue_pv = [&](int t, uint32_t stage, int half, bool first) {
-                const uint32_t d = tmem + 256 * t, b = v_lo + stage * kStep;
-#pragma unroll
-                for (int x = 0; x < 4; x++) {
-                    const int ks = 4 * half + x;
-                    umma_f16_ts(d + 128, d + 8 * ks, b + (uint32_t)((ks * 16 * 128) >> 4), hi_v, E::kIdescO,
-                                (first && ks == 0) ? 0u : 1u);
-                }
+            auto wait_clean = [&](uint32_t stage) {
+                const uint32_t parity = clean_phase >> stage & 1u;
+                clean_phase ^= 1u << stage;
+                return mbar_wait_bounded(&sm.kv_clean[stage], parity);
             };
             for (int r = 0; ok; r++) {
                 PromptUnit u;
@@ -491,62 +505,76 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 mbar_arrive(&sm.unit_free[r & 1]);
                 if (u.n < 0) break;
                 const Span sp(u, tt);
-                const int end = sp.active - 1;  // the tile with the most steps
-                ok = wait_full(ring.stage);
-                for (int t = 0; t < sp.active && ok; t++) {
-                    ok = mbar_wait_bounded(&sm.q_full[t], uses[t] & 1u);
-                    if (!ok) break;
+                const int nst = t == 0 ? sp.steps[0] : sp.steps[1];
+                // S of a step goes over P of the step before, whose PV was issued before it: the
+                // tensor pipe runs one thread's MMAs in order
+                auto issue_s = [&](bool last, bool pass) {
                     tc_fence_after();
-                    issue_s(t, ring.stage);
-                    if (sp.steps[t] == 1) umma_commit(&sm.q_free[t]);
-                }
-                if (!ok) break;
-                umma_commit(&sm.kv_free[ring.stage]);
-                ring.next();
-                for (int i = 0; i < sp.total && ok; i++) {
-                    const Ring v = ring;
+                    const uint32_t b = k_lo + ring.stage * kStep;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++) {
+                        const uint32_t d = (uint32_t)(((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) >> 4);
+                        umma_f16_ss(tm, q_lo + d, hi, b + d, hi, E::kIdescS, ks > 0 ? 1u : 0u);
+                        if (ks == 4 && pass) mbar_arrive(&sm.turn[t ^ 1]);  // the pipe is fed while it wakes
+                    }
+                    umma_commit(&sm.s_full[t]);
+                    umma_commit(&sm.kv_free[ring.stage]);
+                    if (last) umma_commit(&sm.q_free[t]);
                     ring.next();
-                    bool v_seen = false, k_seen = false;
-                    for (int t = 0; t < sp.active && ok; t++) {
-                        if (i >= sp.steps[t]) continue;
-                        ok = mbar_wait_bounded(&sm.p_half[t], p_phase[t]);
-                        if (ok && i == 0 && uses[t] > 0)
-                            ok = mbar_wait_bounded(&sm.o_free[t], (uses[t] - 1) & 1u);
-                        if (ok && !v_seen) {
-                            if (i >= sp.mixed) {
-                                ok = mbar_wait_bounded(&sm.kv_clean[v.stage], clean_phase >> v.stage & 1u);
-                                clean_phase ^= 1u << v.stage;
-                            } else {
-                                ok = wait_full(v.stage);
-                            }
-                            v_seen = true;
-                        }
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_pv(t, v.stage, 0, i == 0);
-                        ok = mbar_wait_bounded(&sm.p_full[t], p_phase[t]);
-                        p_phase[t] ^= 1u;
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_pv(t, v.stage, 1, false);
-                        if (i + 1 == sp.steps[t]) {
-                            umma_commit(&sm.o_full[t]);
-                            uses[t]++;
-                        }
-                        if (t == end) umma_commit(&sm.kv_free[v.stage]);
-                        if (i + 1 < sp.steps[t]) {
-                            // over P of this step: the tensor pipe runs one thread's MMAs in order
-                            if (!k_seen) ok = wait_full(ring.stage);
-                            k_seen = true;
+                };
+                if (nst > 0) {
+                    ok = mbar_wait_bounded(&sm.q_full[t], uses & 1u) && wait_full(ring.stage);
+                    if (!ok) break;
+                    issue_s(nst == 1, false);
+                    if (uses > 0) ok = mbar_wait_bounded(&sm.o_free[t], (uses - 1) & 1u);
+                } else {
+                    ok = wait_full(ring.stage);
+                    if (ok) mbar_arrive(&sm.kv_free[ring.stage]);
+                    ring.next();
+                }
+                for (int i = 0; i < sp.total && ok; i++) {
+                    // O += P(i) V(i), in the parts that the softmax hands over, then S(i + 1); the
+                    // tiles take turns, so that one's softmax runs while the other's MMAs do
+                    const bool live = i < nst, more = i + 1 < nst;
+                    ok = i >= sp.mixed ? wait_clean(ring.stage) : wait_full(ring.stage);
+                    if (live) ok = ok && mbar_wait_bounded(&sm.p_full[t][0], p_phase);
+                    ok = ok && mbar_wait_bounded(&sm.turn[t], turn_phase);
+                    turn_phase ^= 1u;
+                    if (!ok) break;
+                    if (live) {
+                        const uint32_t c = v_lo + ring.stage * kStep;
+#pragma unroll
+                        for (int x = 0; x < kParts; x++) {
+                            if (x > 0) ok = ok && mbar_wait_bounded(&sm.p_full[t][x], p_phase);
                             if (!ok) break;
                             tc_fence_after();
-                            issue_s(t, ring.stage);
-                            if (i + 2 == sp.steps[t]) umma_commit(&sm.q_free[t]);
-                            if (t == end) umma_commit(&sm.kv_free[ring.stage]);
+#pragma unroll
+                            for (int ks = x == 0 ? 0 : 2 + 2 * x; ks < 4 + 2 * x; ks++)
+                                umma_f16_ts(tm + 128, tm + 8 * ks, c + (uint32_t)((ks * 16 * 128) >> 4), hi_v,
+                                            E::kIdescO, i == 0 && ks == 0 ? 0u : 1u);
+                        }
+                        if (!ok) break;
+                        p_phase ^= 1u;
+                        umma_commit(&sm.kv_free[ring.stage]);
+                        if (!more) umma_commit(&sm.o_full[t]);
+                    } else {
+                        mbar_arrive(&sm.kv_free[ring.stage]);
+                    }
+                    ring.next();
+                    if (more) {
+                        ok = wait_full(ring.stage);
+                        if (!ok) break;
+                        issue_s(i + 2 == nst, true);
+                    } else {
+                        mbar_arrive(&sm.turn[t ^ 1]);
+                        if (i + 1 < sp.total) {  // the other tile's K: seen, so that the phases stay in step
+                            ok = wait_full(ring.stage);
+                            if (ok) mbar_arrive(&sm.kv_free[ring.stage]);
+                            ring.next();
                         }
                     }
-                    if (i + 1 < sp.total) ring.next();
                 }
+                uses += nst > 0;
             }
             umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
             if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
@@ -710,7 +738,8 @@ cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t
         !make_map(&mk, BF, k, p.total, p.num_heads, k_stride, 1, kKeys) ||
         !make_map(&mv, BF, p.v, p.total, p.num_heads, p.v_stride, 1, kKeys))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<BF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    auto kernel = p.score_scale < 0.0f ? prompt_attn_kernel<BF, true> : prompt_attn_kernel<BF, false>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(PromptSmem));
     if (e != cudaSuccess) return e;
     // at most one CTA per SM, and no more than there can be units
@@ -718,7 +747,7 @@ cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t
     const int64_t by_max = (int64_t)p.num_seqs * ((p.max_n + ut - 1) / ut), by_total = p.total / ut + p.num_seqs;
     const int64_t units = (by_max < by_total ? by_max : by_total) * p.num_heads;
     const int grid = units < num_sms ? (int)units : num_sms;
-    return launch_plain(prompt_attn_kernel<BF>, dim3((unsigned)grid), dim3(kPromptThreads), sizeof(PromptSmem), s, p,
+    return launch_plain(kernel, dim3((unsigned)grid), dim3(kPromptThreads), sizeof(PromptSmem), s, p,
                         mq, mk, mv);
 }
 
