@@ -298,7 +298,11 @@ kvq_status kvq_prompt_attention(kvq_dtype dtype, const uint16_t *q, int64_t q_ro
     p.max_n = max_tokens_per_seq;
     p.total = total_tokens;
     p.score_scale = softmax_scale * 1.4426950408889634f;
-    p.tile_tokens = 128 / g;
+    p.tile_heads = g % 2 ? g : g / 2;
+    p.tile_tokens = 128 / p.tile_heads;
+    p.tile1_head = g % 2 ? 0 : p.tile_heads;
+    p.tile1_token = g % 2 ? p.tile_tokens : 0;
+    p.unit_tokens = g % 2 ? 2 * p.tile_tokens : p.tile_tokens;
     return from_cuda(kvq::launch_prompt(dtype, p, q, q_row_stride, k, k_row_stride, device_sms(),
                                         reinterpret_cast<cudaStream_t>(stream)));
 }

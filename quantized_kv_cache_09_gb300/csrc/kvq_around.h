@@ -23,7 +23,9 @@ struct PromptParams {
     int num_seqs, num_heads, num_q_heads, group, max_n;
     int64_t total;
     float score_scale;  // softmax_scale * log2(e)
-    int tile_tokens;    // tokens of a 128-row tile: 128 / group
+    // a unit's two tiles of up to 128 rows = tile_tokens x tile_heads, tile 1 tile1_token tokens
+    // and tile1_head heads after tile 0 (one of them 0)
+    int tile_heads, tile_tokens, tile1_head, tile1_token, unit_tokens;
 };
 
 struct PageWeightsParams {

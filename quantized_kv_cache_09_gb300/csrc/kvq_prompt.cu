@@ -10,9 +10,11 @@
 // read about once from HBM): tcgen05 with S, P and O in tensor memory, operands
 // brought by TMA.  One CTA per SM stays resident and takes units in turn; a unit
 // is two tiles of 128 query rows of one (sequence, cache head).  A tile's rows
-// are tile_tokens = 128 / g tokens x the g query heads of the group (row = token
-// * g + head), so that a group of any size reads its cache head's keys once and
-// short prompts fill the tile with heads.  Keys go in steps of 128.
+// are tokens x query heads of the group (row = token * heads + head), so that a
+// group of any size reads its cache head's keys once and short prompts fill the
+// tile with heads: an even group's tiles share the tokens, half of the heads
+// each; an odd group's tiles have all heads of neighbouring tokens.  Keys go in
+// steps of 128.
 //
 // Roles (warps), handing over through mbarriers:
 //   0-3, 4-7  softmax of tile 0, tile 1: one thread per query row.  A row of S
@@ -62,8 +64,8 @@ constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 // a softmax scale of 0 scores 1e-38 * raw instead, so that a masked score stays -inf
 constexpr float kMinScale = 1.17549435e-38f;
-// registers per thread after the split: 2 * 184 + 80 + 64 = 4 * 128, the launch's
-constexpr int kRegsSoftmax = 184, kRegsEpilogue = 80, kRegsIssue = 64;
+// registers per thread after the split: 2 * 176 + 104 + 56 = 4 * 128, the launch's
+constexpr int kRegsSoftmax = 176, kRegsEpilogue = 104, kRegsIssue = 56;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsIssue <= 4 * (65536 / kPromptThreads), "register split");
 
 template <int N>
@@ -131,11 +133,12 @@ struct Span {
     int steps[kUnitTiles];  // key steps of a tile
     int total;              // of the unit
     int mixed;              // first step with keys past some row's position
-    __device__ __forceinline__ Span(const PromptUnit &u, int tile_tokens)
+    __device__ __forceinline__ Span(const PromptUnit &u, const PromptParams &p)
     {
-        active = u.n - u.tok0 > tile_tokens ? 2 : 1;
-        steps[0] = (min(u.tok0 + tile_tokens, u.n) - 1) / kKeys + 1;
-        steps[1] = active == 2 ? (min(u.tok0 + 2 * tile_tokens, u.n) - 1) / kKeys + 1 : 0;
+        const int t1 = u.tok0 + p.tile1_token;  // tile 1's first token
+        active = u.n > t1 ? 2 : 1;
+        steps[0] = (min(u.tok0 + p.tile_tokens, u.n) - 1) / kKeys + 1;
+        steps[1] = active == 2 ? (min(t1 + p.tile_tokens, u.n) - 1) / kKeys + 1 : 0;
         total = max(steps[0], steps[1]);
         mixed = (u.tok0 + 1) / kKeys;
     }
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_prompt[];
     PromptSmem &sm = *reinterpret_cast<PromptSmem *>(smem_prompt);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = p.group, tt = p.tile_tokens;
+    const int G = p.group, tt = p.tile_tokens, th = p.tile_heads;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
@@ -266,10 +269,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 break;
             }
             if (u.n < 0) break;
-            const Span sp(u, tt);
+            const Span sp(u, p);
             if (t >= sp.active) continue;
-            const int nst = sp.steps[t], tok_t = u.tok0 + t * tt;
-            const int pos = row < G * tt ? tok_t + row / G : -1;
+            const int nst = sp.steps[t], tok_t = u.tok0 + t * p.tile1_token;
+            const int pos = row < th * tt ? tok_t + row / th : -1;
             float m_used = -INFINITY;
             uint64_t l2 = pk2(0.0f, 0.0f);
             for (int i = 0; i < nst; i++) {
@@ -388,7 +391,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 break;
             }
             if (u.n < 0) break;
-            const Span sp(u, tt);
+            const Span sp(u, p);
             bool wild = false;
             for (int i = 0; i < sp.total && ok; i++) {
                 ring.next();
@@ -429,47 +432,38 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tc_fence_after();
                 const float2 ml = sm.ml[t][row];
                 const float inv = 1.0f / ml.y;
-                const int tok = u.tok0 + t * tt + row / G, hq = u.h * G + row % G;
-                const bool live = row < G * tt && tok < u.n;
+                const int tok = u.tok0 + t * p.tile1_token + row / th, hq = u.h * G + t * p.tile1_head + row % th;
+                const bool live = row < th * tt && tok < u.n;
                 const int64_t at = (int64_t)(u.c0 + tok) * p.num_q_heads + hq;
+                uint32_t o[64];
 #pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    uint32_t o[32];
+                for (int c = 0; c < 4; c++) {
+                    uint32_t x[32];
+                    tmem_ld32_async(lane_tm + 256 * t + 128 + 32 * c, x);
+                    tmem_ld_wait();
+                    if (wild && live) {
+                        // values that are not finite, of the keys this row sees in the mixed steps
+                        for (int j = sp.mixed * kKeys; j <= tok; j++) {
+                            const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + 32 * c;
 #pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        const int col = 64 * half + 32 * c;
-                        uint32_t x[32];
-                        tmem_ld32_async(lane_tm + 256 * t + 128 + col, x);
-                        tmem_ld_wait();
-                        if (wild && live) {
-                            // values that are not finite, of the keys this row sees in the mixed steps
-                            for (int j = sp.mixed * kKeys; j <= tok; j++) {
-                                const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + col;
-#pragma unroll
-                                for (int e = 0; e < 32; e++) {
-                                    const float y = E::value(vr[e]);
-                                    if (!(fabsf(y) < INFINITY)) x[e] = __float_as_uint(__uint_as_float(x[e]) + y);
-                                }
+                            for (int e = 0; e < 32; e++) {
+                                const float y = E::value(vr[e]);
+                                if (!(fabsf(y) < INFINITY)) x[e] = __float_as_uint(__uint_as_float(x[e]) + y);
                             }
                         }
+                    }
 #pragma unroll
-                        for (int e = 0; e < 16; e++)
-                            o[16 * c + e] =
-                                E::pack(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
-                    }
-                    if (half == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm.o_free[t]);
-                    }
-                    if (live) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * kHeadDim + 64 * half);
-#pragma unroll
-                        for (int c = 0; c < 8; c++)
-                            dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
-                    }
+                    for (int e = 0; e < 16; e++)
+                        o[16 * c + e] = E::pack(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
                 }
+                // O may be written again before this one's stores, which take far longer than its loads
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.o_free[t]);
                 if (!live) continue;
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * kHeadDim);
+#pragma unroll
+                for (int c = 0; c < 16; c++) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 if (p.lse) p.lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
             }
         }
@@ -504,7 +498,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (!fetch(r, u)) break;
                 mbar_arrive(&sm.unit_free[r & 1]);
                 if (u.n < 0) break;
-                const Span sp(u, tt);
+                const Span sp(u, p);
                 const int nst = t == 0 ? sp.steps[0] : sp.steps[1];
                 // S of a step goes over P of the step before, whose PV was issued before it: the
                 // tensor pipe runs one thread's MMAs in order
@@ -538,8 +532,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     const bool live = i < nst, more = i + 1 < nst;
                     ok = i >= sp.mixed ? wait_clean(ring.stage) : wait_full(ring.stage);
                     if (live) ok = ok && mbar_wait_bounded(&sm.p_full[t][0], p_phase);
-                    ok = ok && mbar_wait_bounded(&sm.turn[t], turn_phase);
-                    turn_phase ^= 1u;
+                    const bool both = i < min(sp.steps[0], sp.steps[1]);
+                    if (both) {
+                        ok = ok && mbar_wait_bounded(&sm.turn[t], turn_phase);
+                        turn_phase ^= 1u;
+                    }
                     if (!ok) break;
                     if (live) {
                         const uint32_t c = v_lo + ring.stage * kStep;
@@ -564,9 +561,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (more) {
                         ok = wait_full(ring.stage);
                         if (!ok) break;
-                        issue_s(i + 2 == nst, true);
+                        issue_s(i + 2 == nst, both);
                     } else {
-                        mbar_arrive(&sm.turn[t ^ 1]);
+                        if (both) mbar_arrive(&sm.turn[t ^ 1]);
                         if (i + 1 < sp.total) {  // the other tile's K: seen, so that the phases stay in step
                             ok = wait_full(ring.stage);
                             if (ok) mbar_arrive(&sm.kv_free[ring.stage]);
@@ -580,7 +577,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
         } else if (warp == 13) {
             // ---- units and copies ----
-            const int H = p.num_heads, ut = kUnitTiles * tt;
+            const int H = p.num_heads, ut = p.unit_tokens;
             // a sequence's length, 0 where its bounds are broken
             auto length = [&](int b) {
                 const int c0 = p.cu[b], n = p.cu[b + 1] - c0;
@@ -640,7 +637,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 if (u.n < 0) break;
                 if (lane == 0) {
-                    const Span sp(u, tt);
+                    const Span sp(u, p);
                     auto stage = [&](const CUtensorMap *map, int key, bool raw) {
                         if (used >= kStages) ok = mbar_wait_bounded(&sm.kv_free[ring.stage], ring.phase ^ 1u);
                         if (!ok) return;
@@ -663,10 +660,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         for (int t = 0; i == 0 && t < sp.active && ok; t++) {
                             if (uses[t] > 0) ok = mbar_wait_bounded(&sm.q_free[t], (uses[t] - 1) & 1u);
                             if (!ok) break;
-                            mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * G * tt);
-                            const int tok = u.c0 + u.tok0 + t * tt;
-                            tma_load_3d(sm.q[t], &map_q, 0, u.h * G, tok, &sm.q_full[t]);
-                            tma_load_3d(sm.q[t] + kTileBytes / 2, &map_q, 64, u.h * G, tok, &sm.q_full[t]);
+                            mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * th * tt);
+                            const int tok = u.c0 + u.tok0 + t * p.tile1_token, hq = u.h * G + t * p.tile1_head;
+                            tma_load_3d(sm.q[t], &map_q, 0, hq, tok, &sm.q_full[t]);
+                            tma_load_3d(sm.q[t] + kTileBytes / 2, &map_q, 64, hq, tok, &sm.q_full[t]);
                             uses[t]++;
                         }
                         if (ok) stage(&map_v, i * kKeys, i >= sp.mixed);
@@ -734,7 +731,7 @@ cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t
 {
     CUtensorMap mq, mk, mv;
     if (!encode_tiled()) return cudaErrorNotSupported;
-    if (!make_map(&mq, BF, q, p.total, p.num_q_heads, q_stride, p.group, p.tile_tokens) ||
+    if (!make_map(&mq, BF, q, p.total, p.num_q_heads, q_stride, p.tile_heads, p.tile_tokens) ||
         !make_map(&mk, BF, k, p.total, p.num_heads, k_stride, 1, kKeys) ||
         !make_map(&mv, BF, p.v, p.total, p.num_heads, p.v_stride, 1, kKeys))
         return cudaErrorInvalidValue;
@@ -743,7 +740,7 @@ cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t
                                          (int)sizeof(PromptSmem));
     if (e != cudaSuccess) return e;
     // at most one CTA per SM, and no more than there can be units
-    const int64_t ut = kUnitTiles * p.tile_tokens;
+    const int64_t ut = p.unit_tokens;
     const int64_t by_max = (int64_t)p.num_seqs * ((p.max_n + ut - 1) / ut), by_total = p.total / ut + p.num_seqs;
     const int64_t units = (by_max < by_total ? by_max : by_total) * p.num_heads;
     const int grid = units < num_sms ? (int)units : num_sms;
