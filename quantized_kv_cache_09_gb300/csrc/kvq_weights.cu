@@ -11,11 +11,11 @@
 // so one pass over the codes that keeps a single number per (query row, page)
 // is enough:
 //   page_lse_kernel   one warp per page of 64 keys of one cache head: the codes
-//                     go straight into registers, are widened exactly to fp16
-//                     and multiplied with the query rows as the 8-column
-//                     operand of mma.sync (query rows of the group and of the
-//                     chunk share a page's widening); a page's row maximum and
-//                     sum stay in registers, S goes to the workspace.
+//                     come by bulk copies, are widened exactly to fp16 in
+//                     registers and multiplied with the query rows as the
+//                     8-column operand of mma.sync (query rows of the group and
+//                     of the chunk share a page's widening); a page's row
+//                     maximum and sum stay in registers, S goes to the workspace.
 //   page_sum_kernel   rows of one sequence: log2-sum over the pages, then the
 //                     page masses summed over the rows in a fixed order (no
 //                     atomics: equal inputs give equal bits).
@@ -28,8 +28,28 @@ namespace kvq {
 
 namespace {
 
-constexpr int kPwWarps = 8;
-constexpr int kSumThreads = 256;
+constexpr int kPwWarps = 16;
+constexpr int kPwStages = 3;
+constexpr int kPwChunk = 4096;
+constexpr int kSumThreads = 512;
+
+// the byte formats' exact widening to fp16 pairs
+template <int FMT>
+__device__ __forceinline__ void widen_bytes(uint32_t w, __half2 c[2])
+{
+    if constexpr (FMT == KVQ_FP8_E4M3)
+        widen_e4m3(w, c);
+    else
+        widen_int8(w, c);
+}
+
+// the largest of three binary32 values (one instruction)
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // what a sequence brings: its chunk's first row, rows, length; false (and flagged) when a bound is broken
 struct PwSeq {
@@ -62,9 +82,8 @@ struct Nibbles {
 }  // namespace
 
 // A chunk is 4 KiB of codes: 64 keys (int4, a page) or 32 keys (int8, FP8, half a page) =
-// kTiles tiles of 16.  Lane (g, t) = (lane / 4, lane % 4) holds rows g and g + 8 of each
-// tile, of each row the 16-byte pieces that the k index of the MMA is permuted for: a
-// warp's load covers whole 64-byte runs of 8 rows.
+// kTiles tiles of 16.  Lane (g, t) = (lane / 4, lane % 4) reads of rows g and g + 8 of each
+// tile the 16-byte pieces that the k index of the MMA is permuted for.
 template <int FMT>
 struct PwFmt {
     static constexpr int kRowBytes = FMT == KVQ_INT4_B64 ? 64 : 128;
@@ -73,15 +92,44 @@ struct PwFmt {
     static constexpr int kChunks = kPieces;         // chunks per page
 };
 
+// D = A * B, m16n8k16, fp16 operands, fp32 result (no accumulator to clear first)
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+struct PwSmem {
+    uint8_t ring[kPwWarps][kPwStages][kPwChunk];
+    uint64_t full[kPwWarps][kPwStages];
+    int64_t upto[kMaxSeqsPerLaunch + 1];
+};
+
+// Up to 8 NT query rows of one cache head.  A persistent warp owns a contiguous range of units
+// (pages, the fastest index) and streams their chunks through its own ring of bulk copies.
 template <int FMT, int NT>
-__global__ void __launch_bounds__(kPwWarps * 32) page_lse_kernel(PageWeightsParams p)
+__global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsParams p)
 {
     using F = PwFmt<FMT>;
     constexpr int kCols = 8 * NT;  // query rows per unit
-    __shared__ int64_t upto[kMaxSeqsPerLaunch + 1];
+    extern __shared__ __align__(128) uint8_t smem_pw[];
+    PwSmem &sm = *reinterpret_cast<PwSmem *>(smem_pw);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int H = p.num_heads, G = p.group;
+    pdl_launch_dependents();
+    if (lane < kPwStages) mbar_init(&sm.full[warp][lane], 1);
+    mbar_init_fence();
     // units of sequence b: (cache head, block of kCols query rows, page), the page fastest
     if (warp == 0) {
         int64_t run = 0;
@@ -99,222 +147,311 @@ __global__ void __launch_bounds__(kPwWarps * 32) page_lse_kernel(PageWeightsPara
                 const int64_t v = __shfl_up_sync(kFull, u, o);
                 if (lane >= o) u += v;
             }
-            if (b0 + lane < p.num_seqs) upto[b0 + lane + 1] = run + u;
+            if (b0 + lane < p.num_seqs) sm.upto[b0 + lane + 1] = run + u;
             run += __shfl_sync(kFull, u, 31);
         }
-        if (lane == 0) upto[0] = 0;
+        if (lane == 0) sm.upto[0] = 0;
     }
     __syncthreads();
-    const int64_t U = upto[p.num_seqs];
+    const int64_t U = sm.upto[p.num_seqs];
     const int64_t warps = (int64_t)gridDim.x * kPwWarps, id = (int64_t)warp * gridDim.x + blockIdx.x;
-    int64_t u = U * id / warps;
-    const int64_t end = U * (id + 1) / warps;
+    const int64_t first = U * id / warps;
+    const int units = (int)(U * (id + 1) / warps - first);
     const Nibbles nib;
 
-    while (u < end) {
-        // ---- one segment: pages [j0, j1) of one (sequence, cache head, row block) ----
+    // the place of unit u: its sequence (and what it brings), (head, row block) and page
+    struct Place {
+        PwSeq s;
+        int b, h, row0, j;
+    };
+    auto place = [&](int64_t u) {
+        Place x;
         int lo = 0, hi = p.num_seqs;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (upto[mid] <= u)
+            if (sm.upto[mid] <= u)
                 lo = mid;
             else
                 hi = mid;
         }
-        const int b = lo;
-        PwSeq s;
-        pw_seq(p, b, s);
-        const int np = (s.L + kPage - 1) / kPage;
-        const int rows = s.n * G, blocks = (rows + kCols - 1) / kCols;
-        const int64_t r = u - upto[b];
-        const int j0 = (int)(r % np);
-        const int64_t hr = r / np;
-        const int h = (int)(hr / blocks), row0 = (int)(hr % blocks) * kCols;
-        const int j1 = (int)min((int64_t)np, j0 + (end - u));
-        u += j1 - j0;
-        const int32_t *bt = p.block_table + (int64_t)b * p.max_blocks;
+        x.b = lo;
+        pw_seq(p, lo, x.s);
+        const int np = (x.s.L + kPage - 1) / kPage, blocks = (x.s.n * G + kCols - 1) / kCols;
+        const int64_t r = u - sm.upto[lo], hr = r / np;
+        x.j = (int)(r - hr * np);
+        x.h = (int)(hr / blocks);
+        x.row0 = (int)(hr % blocks) * kCols;
+        return x;
+    };
 
-        // the unit's query rows as the B operand: column g of tile nt is row row0 + 8 nt + g
-        uint32_t qb[NT][8][2];
-        float bias[NT][2];  // columns 2t, 2t + 1: minus the offset share of every raw score (int4)
-        float *dst[NT][2];  // their rows of the workspace
+    // the warp's next 64 units by lane, in two rings of 32 (one is loaded while the other is
+    // used): (page, head) of the codes, key scale, page number
+    uint32_t ph[2] = {0u, 0u};
+    float sk[2] = {0.0f, 0.0f};
+    int pj[2] = {0, 0};
+    auto look = [&](int i, uint32_t &ph_, float &sk_, int &pj_) {
+        if (i + lane >= units) return;
+        const Place x = place(first + i + lane);
+        int pg = p.block_table[(int64_t)x.b * p.max_blocks + x.j];
+        if (pg < 0 || pg >= p.num_pages) {
+            set_flag(p.status, KVQ_FLAG_BAD_PAGE);
+            pg = 0;
+        }
+        ph_ = (uint32_t)pg * (uint32_t)H + (uint32_t)x.h;
+        sk_ = p.k_scales[ph_];
+        pj_ = x.j;
+    };
+    look(0, ph[0], sk[0], pj[0]);
+    look(32, ph[1], sk[1], pj[1]);
+    const int chunks = units * F::kChunks;
+    uint8_t *ring = sm.ring[warp][0];
+    uint64_t *full = sm.full[warp];
+    // bring chunk c into its stage (the ring that holds its unit is picked by a branch: a select
+    // would wait for the other ring's loads)
+    auto bring = [&](int c) {
+        if (c >= chunks) return;
+        const int i = c / F::kChunks, x = c % F::kChunks;
+        const uint32_t at = i & 32 ? __shfl_sync(kFull, ph[1], i & 31) : __shfl_sync(kFull, ph[0], i & 31);
+        if (lane == 0) {
+            const int st = c % kPwStages;
+            mbar_arrive_expect_tx(&full[st], kPwChunk);
+            bulk_copy_g2s(ring + st * kPwChunk,
+                          p.k_codes + (size_t)at * (kPage * F::kRowBytes) + (size_t)x * kPwChunk, kPwChunk, &full[st]);
+        }
+    };
+    __syncwarp();
+    for (int c = 0; c < kPwStages; c++) bring(c);
+
+    uint32_t qb[NT][8][2];       // the unit's query rows as the B operand: column g of tile nt is row row0 + 8 nt + g
+    float bias[NT][2];           // columns 2t, 2t + 1: minus the offset share of every raw score (int4)
+    float *dst[NT][2];           // their rows of the workspace
+    int pos[NT][2], pos0 = 0;    // their positions; the least position of the chunk
+    const float sign = p.score_scale < 0.0f ? -1.0f : 1.0f;
+    const float sabs = fmaxf(fabsf(p.score_scale), 1.17549435e-38f);  // (0 would turn a masked -inf into NaN)
+    bool ok = true;
+    int c = 0, st = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < units; i++) {
+        if (i > 0 && (i & 31) == 0) {  // this ring's turn: the other looks 32 units ahead of it
+            if (i & 32)
+                look(i + 32, ph[0], sk[0], pj[0]);
+            else
+                look(i + 32, ph[1], sk[1], pj[1]);
+        }
+        float fac;
+        int j;
+        if (i & 32) {
+            fac = __shfl_sync(kFull, sk[1], i & 31);
+            j = __shfl_sync(kFull, pj[1], i & 31);
+        } else {
+            fac = __shfl_sync(kFull, sk[0], i & 31);
+            j = __shfl_sync(kFull, pj[0], i & 31);
+        }
+        fac = fmaxf(fac * sabs, 1.17549435e-38f);
+        if (i == 0 || j == 0) {  // another (sequence, head, row block)
+            const Place x = place(first + i);
+            const int rows = x.s.n * G;
+            pos0 = x.s.L - x.s.n;
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
-            const int rr = row0 + 8 * nt + g;
-            const bool live = rr < rows;
-            const uint16_t *q = p.q + ((int64_t)(s.c0 + rr / G) * p.num_q_heads + h * G + rr % G) * kHeadDim;
-            uint4 v[4];
-            float off = 0.0f;
-#pragma unroll
-            for (int m = 0; m < 4; m++) {
-                v[m] = make_uint4(0u, 0u, 0u, 0u);
-                if (!live) continue;
-                if constexpr (FMT == KVQ_INT4_B64)
-                    v[m] = *reinterpret_cast<const uint4 *>(q + 32 * t + 8 * m);
-                else
-                    v[m] = *reinterpret_cast<const uint4 *>(q + 64 * (m >> 1) + 16 * t + 8 * (m & 1));
-            }
-            if constexpr (FMT == KVQ_INT4_B64) {
-                const __half2 odd = __float2half2_rn(-0.0625f);
-#pragma unroll
-                for (int m = 0; m < 4; m++) {  // a word's 8 elements as pairs (0,4) (1,5) (2,6) (3,7)
-                    const uint32_t e04 = __byte_perm(v[m].x, v[m].z, 0x5410), e15 = __byte_perm(v[m].x, v[m].z, 0x7632);
-                    const uint32_t e26 = __byte_perm(v[m].y, v[m].w, 0x5410), e37 = __byte_perm(v[m].y, v[m].w, 0x7632);
-                    const __half2 o15 = __hmul2(*reinterpret_cast<const __half2 *>(&e15), odd);
-                    const __half2 o37 = __hmul2(*reinterpret_cast<const __half2 *>(&e37), odd);
-                    qb[nt][2 * m][0] = e04;
-                    qb[nt][2 * m][1] = h2_bits(o15);
-                    qb[nt][2 * m + 1][0] = e26;
-                    qb[nt][2 * m + 1][1] = h2_bits(o37);
-                    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&e04));
-                    const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&e26));
-                    const float2 x = __half22float2(o15), y = __half22float2(o37);
-                    off += 8.0f * ((a.x + a.y) + (c.x + c.y)) + 112.0f * ((x.x + x.y) + (y.x + y.y));
-                }
-                off += __shfl_xor_sync(kFull, off, 1);  // the four lanes t hold the row's four slices
-                off += __shfl_xor_sync(kFull, off, 2);
-            } else {
+            for (int nt = 0; nt < NT; nt++) {
+                const int rr = x.row0 + 8 * nt + g;
+                const bool live = rr < rows;
+                const uint16_t *q = p.q + ((int64_t)(x.s.c0 + rr / G) * p.num_q_heads + x.h * G + rr % G) * kHeadDim;
+                const __half2 flip = __float2half2_rn(sign);
+                uint4 v[4];
+                float off = 0.0f;
 #pragma unroll
                 for (int m = 0; m < 4; m++) {
-                    qb[nt][2 * m][0] = v[m].x;
-                    qb[nt][2 * m][1] = v[m].y;
-                    qb[nt][2 * m + 1][0] = v[m].z;
-                    qb[nt][2 * m + 1][1] = v[m].w;
-                }
-            }
+                    v[m] = make_uint4(0u, 0u, 0u, 0u);
+                    if (!live) continue;
+                    if constexpr (FMT == KVQ_INT4_B64)
+                        v[m] = *reinterpret_cast<const uint4 *>(q + 32 * t + 8 * m);
+                    else
+                        v[m] = *reinterpret_cast<const uint4 *>(q + 64 * (m >> 1) + 16 * t + 8 * (m & 1));
+                    uint32_t *w = reinterpret_cast<uint32_t *>(&v[m]);
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-                bias[nt][e] = -__shfl_sync(kFull, off, (2 * t + e) * 4);
-                const int rc = row0 + 8 * nt + 2 * t + e;
-                dst[nt][e] = rc < rows ? p.lse + ((int64_t)(s.c0 + rc / G) * p.num_q_heads + h * G + rc % G) *
-                                                     p.max_blocks
-                                       : nullptr;
+                    for (int e = 0; e < 4; e++) w[e] = h2_bits(__hmul2(*reinterpret_cast<__half2 *>(&w[e]), flip));
+                }
+                if constexpr (FMT == KVQ_INT4_B64) {
+                    const __half2 odd = __float2half2_rn(-0.0625f);
+#pragma unroll
+                    for (int m = 0; m < 4; m++) {  // a word's 8 elements as pairs (0,4) (1,5) (2,6) (3,7)
+                        const uint32_t e04 = __byte_perm(v[m].x, v[m].z, 0x5410);
+                        const uint32_t e15 = __byte_perm(v[m].x, v[m].z, 0x7632);
+                        const uint32_t e26 = __byte_perm(v[m].y, v[m].w, 0x5410);
+                        const uint32_t e37 = __byte_perm(v[m].y, v[m].w, 0x7632);
+                        const __half2 o15 = __hmul2(*reinterpret_cast<const __half2 *>(&e15), odd);
+                        const __half2 o37 = __hmul2(*reinterpret_cast<const __half2 *>(&e37), odd);
+                        qb[nt][2 * m][0] = e04;
+                        qb[nt][2 * m][1] = h2_bits(o15);
+                        qb[nt][2 * m + 1][0] = e26;
+                        qb[nt][2 * m + 1][1] = h2_bits(o37);
+                        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&e04));
+                        const float2 d = __half22float2(*reinterpret_cast<const __half2 *>(&e26));
+                        const float2 e = __half22float2(o15), y = __half22float2(o37);
+                        off += 8.0f * ((a.x + a.y) + (d.x + d.y)) + 112.0f * ((e.x + e.y) + (y.x + y.y));
+                    }
+                    off += __shfl_xor_sync(kFull, off, 1);  // the four lanes t hold the row's four slices
+                    off += __shfl_xor_sync(kFull, off, 2);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 4; m++) {
+                        qb[nt][2 * m][0] = v[m].x;
+                        qb[nt][2 * m][1] = v[m].y;
+                        qb[nt][2 * m + 1][0] = v[m].z;
+                        qb[nt][2 * m + 1][1] = v[m].w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    bias[nt][e] = -__shfl_sync(kFull, off, (2 * t + e) * 4);
+                    const int rc = x.row0 + 8 * nt + 2 * t + e;
+                    dst[nt][e] = rc < rows ? p.lse + ((int64_t)(x.s.c0 + rc / G) * p.num_q_heads + x.h * G + rc % G) *
+                                                         p.max_blocks
+                                           : nullptr;
+                    pos[nt][e] = pos0 + rc / G;
+                }
             }
         }
 
-        // page ids and key scales of 32 pages at a time, lane l those of page ring0 + l
-        int ring0 = j0, pg = 0;
-        float sk = 0.0f;
-        auto ring = [&](int j) {
-            ring0 = j;
-            if (j + lane < j1) {
-                pg = bt[j + lane];
-                if (pg < 0 || pg >= p.num_pages) {
-                    set_flag(p.status, KVQ_FLAG_BAD_PAGE);
-                    pg = 0;
-                }
-                sk = p.k_scales[(int64_t)pg * H + h];
+        // raw scores of the page: acc[tile][nt] = rows g, g + 8 of the tile x columns 2t, 2t + 1
+        float acc[4][NT][4];
+#pragma unroll
+        for (int x = 0; x < F::kChunks; x++, c++) {
+            if (!mbar_wait_bounded(&full[st], phase)) ok = false;
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            const uint32_t base = smem_addr(ring) + st * kPwChunk + g * F::kRowBytes + 16 * t;
+            uint4 w[8];
+#pragma unroll
+            for (int k = 0; k < 8; k++) {  // (tile, row half, piece)
+                const int tile = k / (2 * F::kPieces), half = k / F::kPieces % 2, piece = k % F::kPieces;
+                w[k] = lds128(base + (16 * tile + 8 * half) * F::kRowBytes + 64 * piece);
             }
-        };
-        // chunk x of the page whose ring lane is l
-        auto load = [&](int page, int x, uint4 (&d)[8]) {
-            const uint8_t *base = p.k_codes + ((size_t)page * H + h) * (kPage * F::kRowBytes) + 4096 * x +
-                                  g * F::kRowBytes + 16 * t;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {  // (tile, row half, piece)
-                const int tile = i / (2 * F::kPieces), half = i / F::kPieces % 2, piece = i % F::kPieces;
-                d[i] = ld_stream_v4(base + (16 * tile + 8 * half) * F::kRowBytes + 64 * piece);
+            if (++st == kPwStages) {
+                st = 0;
+                phase ^= 1u;
             }
-        };
-        ring(j0);
-        uint4 cur[8];
-        load(__shfl_sync(kFull, pg, 0), 0, cur);
-        for (int j = j0; j < j1; j++) {
-            float acc[4][NT][4];
+            __syncwarp();
+            if (lane == 0) fence_proxy_async_smem();
+            bring(c + kPwStages);
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+            for (int pc = 0; pc < F::kPieces; pc++)
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) acc[i][nt][e] = 0.0f;
-            const int page = __shfl_sync(kFull, pg, j - ring0);
-            const float fac = __shfl_sync(kFull, sk, j - ring0) * p.score_scale;
-#pragma unroll
-            for (int x = 0; x < F::kChunks; x++) {
-                uint4 c[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) c[i] = cur[i];
-                if (x + 1 < F::kChunks) {
-                    load(page, x + 1, cur);
-                } else if (j + 1 < j1) {
-                    if (j + 1 - ring0 == 32) ring(j + 1);
-                    load(__shfl_sync(kFull, pg, j + 1 - ring0), 0, cur);
-                }
-#pragma unroll
-                for (int ks = 0; ks < 4; ks++) {
+                for (int ks = 0; ks < 4; ks++)
 #pragma unroll
                     for (int tile = 0; tile < F::kTiles; tile++) {
                         float(&a)[NT][4] = acc[x * F::kTiles + tile];
+                        const uint4 &wa = w[tile * 2 * F::kPieces + pc];
+                        const uint4 &wb = w[tile * 2 * F::kPieces + F::kPieces + pc];
+                        const uint32_t ua = ks == 0 ? wa.x : ks == 1 ? wa.y : ks == 2 ? wa.z : wa.w;
+                        const uint32_t ub = ks == 0 ? wb.x : ks == 1 ? wb.y : ks == 2 ? wb.z : wb.w;
+                        if constexpr (FMT == KVQ_INT4_B64) {
+                            const uint32_t ah = ua >> 8, bh = ub >> 8;
 #pragma unroll
-                        for (int pc = 0; pc < F::kPieces; pc++) {
-                            const uint4 &wa = c[tile * 2 * F::kPieces + pc];
-                            const uint4 &wb = c[tile * 2 * F::kPieces + F::kPieces + pc];
-                            const uint32_t ua = ks == 0 ? wa.x : ks == 1 ? wa.y : ks == 2 ? wa.z : wa.w;
-                            const uint32_t ub = ks == 0 ? wb.x : ks == 1 ? wb.y : ks == 2 ? wb.z : wb.w;
-                            if constexpr (FMT == KVQ_INT4_B64) {
-                                const uint32_t ah = ua >> 8, bh = ub >> 8;
+                            for (int nt = 0; nt < NT; nt++) {
+                                const uint32_t(&q)[8][2] = qb[nt];
+                                if (ks == 0)
+                                    mma16816_first(a[nt], nib.lo(ua), nib.lo(ub), nib.hi(ua), nib.hi(ub), q[0][0],
+                                                   q[0][1]);
+                                else
+                                    mma16816(a[nt], nib.lo(ua), nib.lo(ub), nib.hi(ua), nib.hi(ub), q[2 * ks][0],
+                                             q[2 * ks][1]);
+                                mma16816(a[nt], nib.lo(ah), nib.lo(bh), nib.hi(ah), nib.hi(bh), q[2 * ks + 1][0],
+                                         q[2 * ks + 1][1]);
+                            }
+                        } else {
+                            __half2 ra[2], rb[2];
+                            widen_bytes<FMT>(ua, ra);
+                            widen_bytes<FMT>(ub, rb);
 #pragma unroll
-                                for (int nt = 0; nt < NT; nt++) {
-                                    mma16816(a[nt], nib.lo(ua), nib.lo(ub), nib.hi(ua), nib.hi(ub),
-                                             qb[nt][2 * ks][0], qb[nt][2 * ks][1]);
-                                    mma16816(a[nt], nib.lo(ah), nib.lo(bh), nib.hi(ah), nib.hi(bh),
-                                             qb[nt][2 * ks + 1][0], qb[nt][2 * ks + 1][1]);
-                                }
-                            } else {
-                                __half2 ra[2], rb[2];
-                                if constexpr (FMT == KVQ_FP8_E4M3) {
-                                    widen_e4m3(ua, ra);
-                                    widen_e4m3(ub, rb);
-                                } else {
-                                    widen_int8(ua, ra);
-                                    widen_int8(ub, rb);
-                                }
-#pragma unroll
-                                for (int nt = 0; nt < NT; nt++)
+                            for (int nt = 0; nt < NT; nt++) {
+                                const uint32_t(&q)[2] = qb[nt][4 * pc + ks];
+                                if (pc == 0 && ks == 0)
+                                    mma16816_first(a[nt], h2_bits(ra[0]), h2_bits(rb[0]), h2_bits(ra[1]),
+                                                   h2_bits(rb[1]), q[0], q[1]);
+                                else
                                     mma16816(a[nt], h2_bits(ra[0]), h2_bits(rb[0]), h2_bits(ra[1]), h2_bits(rb[1]),
-                                             qb[nt][4 * pc + ks][0], qb[nt][4 * pc + ks][1]);
+                                             q[0], q[1]);
                             }
                         }
                     }
-                }
+        }
+        if (!ok) break;
+
+        // log2-sum of the page per query row: lanes (0..7, t) hold the 64 keys of columns 2t, 2t + 1
+        const int k0 = j * kPage;
+        if (k0 + kPage - 1 > pos0) {  // keys past some row's position
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (k0 + 16 * k + 8 * (e >> 1) + g > pos[nt][e & 1]) acc[k][nt][e] = -INFINITY;
+        }
+        const float f = FMT == KVQ_INT4_B64 ? fac * 16777216.0f : fac;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            float m[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                m[e] = max3(acc[0][nt][e], acc[0][nt][2 + e], acc[1][nt][e]);
+                m[e] = max3(m[e], acc[1][nt][2 + e], acc[2][nt][e]);
+                m[e] = max3(m[e], acc[2][nt][2 + e], acc[3][nt][e]);
+                m[e] = fmaxf(m[e], acc[3][nt][2 + e]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(kFull, m[e], o));
             }
-            // log2-sum of the page per query row; lanes (0..7, t) hold the rows 2t, 2t + 1 of a tile
-            const int k0 = j * kPage;
-            const bool cut = k0 + kPage - 1 > s.L - s.n;  // keys past some row's position
+            // 2^(s - m) with s - m = f (raw - raw max): the columns' pair in one instruction.  A row
+            // whose keys are all masked keeps a sum of 0
+            const uint64_t f2 = pk2(f, f);
+            const uint64_t r2 = pk2(m[0] == -INFINITY ? 0.0f : -f * m[0], m[1] == -INFINITY ? 0.0f : -f * m[1]);
+            uint64_t l2 = pk2(0.0f, 0.0f);
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    float v[8], m = -INFINITY;
-                    const int pos = s.L - s.n + (row0 + 8 * nt + 2 * t + e) / G;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float raw = acc[i >> 1][nt][2 * (i & 1) + e];
-                        v[i] = FMT == KVQ_INT4_B64 ? fmaf(raw, fac * 16777216.0f, bias[nt][e] * fac) : raw * fac;
-                        if (cut && k0 + 16 * (i >> 1) + 8 * (i & 1) + g > pos) v[i] = -INFINITY;
-                        m = fmaxf(m, v[i]);
-                    }
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                    const float ref = m == -INFINITY ? 0.0f : m;
-                    float l = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 8; i++) l += ex2_approx(v[i] - ref);
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
-                    if (g == 0 && dst[nt][e]) dst[nt][e][j] = m == -INFINITY ? m : m + __log2f(l);
-                }
+            for (int k = 0; k < 8; k++) {
+                float x0, x1;
+                upk2(fma2(pk2(acc[k >> 1][nt][2 * (k & 1)], acc[k >> 1][nt][2 * (k & 1) + 1]), f2, r2), x0, x1);
+                l2 = add2(l2, pk2(ex2_approx(x0), ex2_approx(x1)));
+            }
+            // sums over the 8 lanes of a column: the first exchange leaves column 2t to even g, 2t + 1
+            // to odd g
+            float la, lb;
+            upk2(l2, la, lb);
+            const bool odd = g & 1;
+            float l = odd ? lb : la;
+            l += __shfl_xor_sync(kFull, odd ? la : lb, 4);
+            l += __shfl_xor_sync(kFull, l, 8);
+            l += __shfl_xor_sync(kFull, l, 16);
+            float *d = odd ? dst[nt][1] : dst[nt][0];
+            const float mm = odd ? m[1] : m[0], bb = odd ? bias[nt][1] : bias[nt][0];
+            if (g < 2 && d) d[j] = fmaf(f, mm, FMT == KVQ_INT4_B64 ? bb * fac : 0.0f) + __log2f(l);
+        }
+    }
+    if (!ok) {  // a copy did not come: flagged, and none is left in flight
+        if (lane == 0) set_flag(p.status, KVQ_FLAG_TIMEOUT);
+        for (int k = 0; k < kPwStages && c + k < chunks; k++) {
+            mbar_wait_bounded(&full[st], phase);
+            if (++st == kPwStages) {
+                st = 0;
+                phase ^= 1u;
+            }
         }
     }
 }
 
 // Rows [64 c, 64 c + 64) of sequence b (query rows, tokens x heads): the rows' log2-sums over
-// the pages, then each page's mass over these rows, to the output (one chunk) or to `part`.
+// the pages (one pass: maximum and sum together), then each page's mass over these rows, to the
+// output (one chunk) or to `part`.
 __global__ void __launch_bounds__(kSumThreads) page_sum_kernel(PageWeightsParams p)
 {
+    constexpr int kGroups = 4, kTile = kSumThreads / kGroups;  // a tile of pages x groups of rows
     __shared__ float total[kPwSumRows];
+    __shared__ float sums[kGroups][kTile];
     const int b = blockIdx.y, c = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_launch_dependents();
+    pdl_wait();
     PwSeq s;
     if (!pw_seq(p, b, s)) return;
     const int np = (s.L + kPage - 1) / kPage, mb = p.max_blocks;
@@ -331,36 +468,60 @@ __global__ void __launch_bounds__(kSumThreads) page_sum_kernel(PageWeightsParams
     const float *lse = p.lse + ((int64_t)s.c0 * p.num_q_heads + r0) * mb;
     for (int r = warp; r < nr; r += kSumThreads / 32) {
         const float *x = lse + (int64_t)r * mb;
-        float m = -INFINITY;
-        for (int j = lane; j < np; j += 32) m = fmaxf(m, x[j]);
+        float m = -INFINITY, l = 0.0f;
+        for (int j0 = 0; j0 < np; j0 += 8 * 32) {
+            float v[8], top = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        float l = 0.0f;
-        for (int j = lane; j < np; j += 32) l += ex2_approx(x[j] - m);
+            for (int k = 0; k < 8; k++) v[k] = j0 + 32 * k + lane < np ? x[j0 + 32 * k + lane] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 8; k++) top = fmaxf(top, v[k]);
+            if (top == -INFINITY) continue;
+            l *= ex2_approx(m - top);  // (m = -inf: the sum was 0)
+#pragma unroll
+            for (int k = 0; k < 8; k++) l += ex2_approx(v[k] - top);
+            m = top;
+        }
+        float top = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        l = m == -INFINITY ? 0.0f : l * ex2_approx(m - top);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-        if (lane == 0) total[r] = m + __log2f(l);
+        if (lane == 0) total[r] = top + __log2f(l);
     }
     __syncthreads();
     const bool last = rows <= kPwSumRows;  // the sequence's only chunk
     const int per_token = (p.num_q_heads + kPwSumRows - 1) / kPwSumRows;
     float *part = p.part + ((int64_t)s.c0 * per_token + c) * mb;
-    for (int j = tid; j < (last ? mb : np); j += kSumThreads) {
+    const int grp = tid / kTile, jj = tid % kTile;
+    for (int j0 = 0; j0 < (last ? mb : np); j0 += kTile) {
+        const int j = j0 + jj;
         float a = 0.0f;
         if (j < np) {
-#pragma unroll 8
-            for (int r = 0; r < nr; r++) a += ex2_approx(lse[(int64_t)r * mb + j] - total[r]);
+#pragma unroll
+            for (int k = 0; k < kPwSumRows / kGroups; k++) {
+                const int r = grp * (kPwSumRows / kGroups) + k;
+                if (r < nr) a += ex2_approx(lse[(int64_t)r * mb + j] - total[r]);
+            }
         }
-        if (!last)
-            part[j] = a;
-        else
-            out[j] = j < np ? fmaf(p.decay, in ? in[j] : 0.0f, a) : 0.0f;
+        sums[grp][jj] = a;
+        __syncthreads();
+        if (grp == 0 && j < mb) {
+            a = (sums[0][jj] + sums[1][jj]) + (sums[2][jj] + sums[3][jj]);
+            if (!last) {
+                if (j < np) part[j] = a;
+            } else {
+                out[j] = j < np ? fmaf(p.decay, in ? in[j] : 0.0f, a) : 0.0f;
+            }
+        }
+        __syncthreads();
     }
 }
 
 __global__ void __launch_bounds__(kSumThreads) page_join_kernel(PageWeightsParams p)
 {
     const int b = blockIdx.y, j = blockIdx.x * kSumThreads + threadIdx.x, mb = p.max_blocks;
+    pdl_wait();
     PwSeq s;
     if (!pw_seq(p, b, s) || j >= mb) return;
     const int64_t rows = (int64_t)s.n * p.num_q_heads;
@@ -382,10 +543,10 @@ __global__ void __launch_bounds__(kSumThreads) page_join_kernel(PageWeightsParam
 template <int FMT, int NT>
 static cudaError_t launch_page_lse(const PageWeightsParams &p, int num_sms, cudaStream_t s)
 {
-    int ctas = 0;
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, page_lse_kernel<FMT, NT>, kPwWarps * 32, 0);
+    cudaError_t e = cudaFuncSetAttribute(page_lse_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(PwSmem));
     if (e != cudaSuccess) return e;
-    return launch_plain(page_lse_kernel<FMT, NT>, dim3((unsigned)(num_sms * ctas)), dim3(kPwWarps * 32), 0, s, p);
+    return launch_plain(page_lse_kernel<FMT, NT>, dim3((unsigned)num_sms), dim3(kPwWarps * 32), sizeof(PwSmem), s, p);
 }
 
 template <int FMT>
@@ -393,8 +554,7 @@ static cudaError_t launch_page_weights_fmt(const PageWeightsParams &p, int num_s
 {
     const int64_t rows = (int64_t)p.max_q * p.group;  // query rows of one cache head
     if (rows <= 8) return launch_page_lse<FMT, 1>(p, num_sms, s);
-    if (rows <= 16) return launch_page_lse<FMT, 2>(p, num_sms, s);
-    return launch_page_lse<FMT, 4>(p, num_sms, s);
+    return launch_page_lse<FMT, 2>(p, num_sms, s);
 }
 
 size_t page_weights_lse_floats(int64_t total_q, int num_q_heads, int max_blocks)
@@ -416,9 +576,9 @@ cudaError_t launch_page_weights(int fmt, const PageWeightsParams &p, int num_sms
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.max_q * p.num_q_heads;
     const int64_t chunks = rows == 0 ? 1 : (rows + kPwSumRows - 1) / kPwSumRows;
-    e = launch_plain(page_sum_kernel, dim3((unsigned)chunks, (unsigned)p.num_seqs), dim3(kSumThreads), 0, s, p);
+    e = launch_pdl(page_sum_kernel, dim3((unsigned)chunks, (unsigned)p.num_seqs), dim3(kSumThreads), 0, s, p);
     if (e != cudaSuccess || chunks == 1) return e;
-    return launch_plain(page_join_kernel, dim3((unsigned)((p.max_blocks + kSumThreads - 1) / kSumThreads),
+    return launch_pdl(page_join_kernel, dim3((unsigned)((p.max_blocks + kSumThreads - 1) / kSumThreads),
                                                (unsigned)p.num_seqs),
                         dim3(kSumThreads), 0, s, p);
 }
