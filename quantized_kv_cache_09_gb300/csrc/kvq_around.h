@@ -69,6 +69,7 @@ cudaError_t launch_prompt(int dtype, const PromptParams &p, const uint16_t *q, i
                           int64_t k_stride, int num_sms, cudaStream_t s);
 size_t page_weights_lse_floats(int64_t total_q, int num_q_heads, int max_blocks);
 size_t page_weights_workspace_bytes(int64_t total_q, int num_q_heads, int max_blocks);
+cudaError_t launch_page_window(int fmt, const PageWeightsParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_page_weights(int fmt, const PageWeightsParams &p, int num_sms, cudaStream_t s);
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s);
 

@@ -20,9 +20,7 @@
 //                     page masses summed over the rows in a fixed order (no
 //                     atomics: equal inputs give equal bits).
 //   page_join_kernel  adds the row chunks of long windows.
-#include "kvq_around.h"
-#include "kvq_device.cuh"
-#include "kvq_internal.h"
+#include "kvq_weights.cuh"
 
 namespace kvq {
 
@@ -33,37 +31,6 @@ constexpr int kPwStages = 3;
 constexpr int kPwChunk = 4096;
 constexpr int kSumThreads = 512;
 
-// the byte formats' exact widening to fp16 pairs
-template <int FMT>
-__device__ __forceinline__ void widen_bytes(uint32_t w, __half2 c[2])
-{
-    if constexpr (FMT == KVQ_FP8_E4M3)
-        widen_e4m3(w, c);
-    else
-        widen_int8(w, c);
-}
-
-// the largest of three binary32 values (one instruction)
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-// what a sequence brings: its chunk's first row, rows, length; false (and flagged) when a bound is broken
-struct PwSeq {
-    int c0, n, L;
-};
-__device__ __forceinline__ bool pw_seq(const PageWeightsParams &p, int b, PwSeq &s)
-{
-    s.c0 = p.cu_q[b];
-    s.n = p.cu_q[b + 1] - s.c0;
-    s.L = p.seq_lens[b];
-    return s.n >= 0 && s.n <= p.max_q && s.n <= s.L && s.L <= (int64_t)p.max_blocks * kPage && s.c0 >= 0 &&
-           (int64_t)s.c0 + s.n <= p.total_q;
-}
-
 // int4 codes widened exactly to fp16 subnormals, one lop3 per pair: an even element (low
 // nibble n of its byte, c the signed code) becomes (c + 8) * 2^-24, an odd one
 // (7 - c) * 2^-20; q's odd elements enter as -q / 16, so a raw score is
@@ -72,11 +39,18 @@ struct Nibbles {
     uint32_t m_lo, m_hi, x_lo, x_hi;
     __device__ __forceinline__ Nibbles() : m_lo(0x000f000fu), m_hi(0x00f000f0u), x_lo(0x00080008u), x_hi(0x00700070u)
     {
-        // held in registers, so that (x & m) ^ c is one instruction
+        // held in registers: an instruction takes one immediate
         asm volatile("" : "+r"(m_lo), "+r"(m_hi), "+r"(x_lo), "+r"(x_hi));
     }
-    __device__ __forceinline__ uint32_t lo(uint32_t x) const { return (x & m_lo) ^ x_lo; }
-    __device__ __forceinline__ uint32_t hi(uint32_t x) const { return (x & m_hi) ^ x_hi; }
+    // (x & m) ^ c as one lop3 (written as C, it became two: 531 -> 403 warp instructions a page)
+    static __device__ __forceinline__ uint32_t flip(uint32_t x, uint32_t m, uint32_t c)
+    {
+        uint32_t d;
+        asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(x), "r"(m), "r"(c));
+        return d;
+    }
+    __device__ __forceinline__ uint32_t lo(uint32_t x) const { return flip(x, m_lo, x_lo); }
+    __device__ __forceinline__ uint32_t hi(uint32_t x) const { return flip(x, m_hi, x_hi); }
 };
 
 }  // namespace
@@ -227,7 +201,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     float *dst[NT][2];           // their rows of the workspace
     int pos[NT][2], pos0 = 0;    // their positions; the least position of the chunk
     const float sign = p.score_scale < 0.0f ? -1.0f : 1.0f;
-    const float sabs = fmaxf(fabsf(p.score_scale), 1.17549435e-38f);  // (0 would turn a masked -inf into NaN)
+    const float sabs = fmaxf(fabsf(p.score_scale), kPwMinScale);
     bool ok = true;
     int c = 0, st = 0;
     uint32_t phase = 0;
@@ -247,7 +221,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
             fac = __shfl_sync(kFull, sk[0], i & 31);
             j = __shfl_sync(kFull, pj[0], i & 31);
         }
-        fac = fmaxf(fac * sabs, 1.17549435e-38f);
+        fac = fmaxf(fac * sabs, kPwMinScale);
         if (i == 0 || j == 0) {  // another (sequence, head, row block)
             const Place x = place(first + i);
             const int rows = x.s.n * G;
@@ -466,28 +440,43 @@ __global__ void __launch_bounds__(kSumThreads) page_sum_kernel(PageWeightsParams
     if (r0 >= rows) return;
     const int nr = (int)min((int64_t)kPwSumRows, rows - r0);
     const float *lse = p.lse + ((int64_t)s.c0 * p.num_q_heads + r0) * mb;
-    for (int r = warp; r < nr; r += kSumThreads / 32) {
-        const float *x = lse + (int64_t)r * mb;
-        float m = -INFINITY, l = 0.0f;
-        for (int j0 = 0; j0 < np; j0 += 8 * 32) {
-            float v[8], top = m;
+    constexpr int kRowsWarp = kPwSumRows / (kSumThreads / 32);  // a warp's rows, all in flight at once
+    {
+        float m[kRowsWarp], l[kRowsWarp];
 #pragma unroll
-            for (int k = 0; k < 8; k++) v[k] = j0 + 32 * k + lane < np ? x[j0 + 32 * k + lane] : -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 8; k++) top = fmaxf(top, v[k]);
-            if (top == -INFINITY) continue;
-            l *= ex2_approx(m - top);  // (m = -inf: the sum was 0)
-#pragma unroll
-            for (int k = 0; k < 8; k++) l += ex2_approx(v[k] - top);
-            m = top;
+        for (int i = 0; i < kRowsWarp; i++) {
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
         }
-        float top = m;
+        for (int j0 = 0; j0 < np; j0 += 4 * 32) {
+            float v[kRowsWarp][4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-        l = m == -INFINITY ? 0.0f : l * ex2_approx(m - top);
+            for (int i = 0; i < kRowsWarp; i++)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
-        if (lane == 0) total[r] = top + __log2f(l);
+                for (int k = 0; k < 4; k++) {
+                    const int r = warp * kRowsWarp + i, j = j0 + 32 * k + lane;
+                    v[i][k] = r < nr && j < np ? lse[(int64_t)r * mb + j] : -INFINITY;
+                }
+#pragma unroll
+            for (int i = 0; i < kRowsWarp; i++) {
+                const float top = fmaxf(max3(m[i], v[i][0], v[i][1]), fmaxf(v[i][2], v[i][3]));
+                const float ref = top == -INFINITY ? 0.0f : top;
+                l[i] *= ex2_approx(m[i] - ref);  // (m = -inf: the sum was 0)
+#pragma unroll
+                for (int k = 0; k < 4; k++) l[i] += ex2_approx(v[i][k] - ref);
+                m[i] = top;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRowsWarp; i++) {
+            float top = m[i];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            float a = m[i] == -INFINITY ? l[i] : l[i] * ex2_approx(m[i] - top);  // (l = 0, or NaN)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+            if (lane == 0 && warp * kRowsWarp + i < nr) total[warp * kRowsWarp + i] = top + __log2f(a);
+        }
     }
     __syncthreads();
     const bool last = rows <= kPwSumRows;  // the sequence's only chunk
@@ -554,7 +543,8 @@ static cudaError_t launch_page_weights_fmt(const PageWeightsParams &p, int num_s
 {
     const int64_t rows = (int64_t)p.max_q * p.group;  // query rows of one cache head
     if (rows <= 8) return launch_page_lse<FMT, 1>(p, num_sms, s);
-    return launch_page_lse<FMT, 2>(p, num_sms, s);
+    if (rows <= 16) return launch_page_lse<FMT, 2>(p, num_sms, s);
+    return launch_page_window(FMT, p, num_sms, s);
 }
 
 size_t page_weights_lse_floats(int64_t total_q, int num_q_heads, int max_blocks)

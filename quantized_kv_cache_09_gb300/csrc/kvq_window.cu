@@ -1,0 +1,407 @@
+// kvq_window.cu -- page weights for windows of query rows: more than 16 rows of one cache head
+// (the last tokens of a prompt, chunks).  The same numbers as page_lse_kernel of kvq_weights.cu
+// -- S(row, page) = log2 sum_{t in page} 2^(score) -- on the 5th-generation tensor cores: 128
+// query rows share one widening of a page's codes, and the widening, the MMAs and the softmax
+// sums each run in their own warps.
+//
+// A persistent CTA per SM takes an equal contiguous share of all steps; a step is two pages (128
+// keys) of one (sequence, cache head, tile of 128 query rows).  Roles:
+//   warps 0-3    widening: codes of a step from the copy ring to fp16 in shared memory (128-byte
+//                swizzled, K-major); a new tile's query rows first, in the same layout.  int4 pairs
+//                come out as elements (0,4) (1,5) (2,6) (3,7) of a word, so q is permuted alike
+//   warps 4-11   softmax sums, warps 4-7 the even steps, 8-11 the odd ones: one thread per query
+//                row reads its 64 scores of each page from tensor memory
+//   warp 12      one thread issues the MMAs: S = Q K^T, M = N = 128, four S in tensor memory
+//   warp 13      looks pages up and issues the bulk copies, five steps ahead
+// Every hand-off is an mbarrier, every wait bounded.  With 128 live rows a step costs about as
+// many cycles of the exponential unit (16384 / 32), of the tensor pipe (8 * 64) and of issue.
+#include "kvq_tc.cuh"
+#include "kvq_weights.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kWinThreads = 14 * 32;
+constexpr int kWinRows = 128;
+constexpr int kWinKeys = 2 * kPage;
+constexpr int kCodeStages = 5, kKeyStages = 2, kScoreStages = 4, kMeta = 16;
+// a step's record lives until its sums are done: the copies run at most the sum of the stages ahead
+static_assert(kMeta >= kCodeStages + kKeyStages + kScoreStages + 2, "records outlive their steps");
+constexpr int kWinTile = kWinRows * kHeadDim * 2;
+constexpr uint32_t kWinIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);  // f32 += f16 x f16, M = N = 128
+
+// what a step is: its sequence, cache head, first query row and page, key scales of its pages
+struct WinStep {
+    int32_t c0, n, L, h, row0, j, pages, qbuf;
+    float sk[2];
+    int32_t first, last;  // of its tile's run in this CTA
+};
+
+struct alignas(1024) WinSmem {
+    uint8_t q[2][kWinTile];
+    uint8_t k[kKeyStages][kWinTile];
+    uint8_t code[kCodeStages][2 * kPage * kHeadDim];
+    uint64_t code_full[kCodeStages], code_free[kCodeStages];
+    uint64_t k_full[kKeyStages], k_free[kKeyStages];
+    uint64_t s_full[kScoreStages], s_free[kScoreStages];
+    uint64_t q_free[2], mma_done;
+    WinStep meta[kMeta];
+    int64_t upto[kMaxSeqsPerLaunch + 1];
+    uint32_t tmem;
+};
+static_assert(sizeof(WinSmem) <= 227 * 1024, "one CTA's shared memory");
+
+// byte offset of elements 8c .. 8c + 7 of row r in a K-major tile of 128 rows, 128-byte swizzled
+__device__ __forceinline__ uint32_t tile_chunk(int r, int c)
+{
+    return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ uint32_t lop_and_xor(uint32_t x, uint32_t m, uint32_t c)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(d) : "r"(x), "r"(m), "r"(c));  // (x & m) ^ c
+    return d;
+}
+
+// 8 int4 codes (a word) as fp16, pairs (0,4) (1,5) (2,6) (3,7): a nibble with its top bit flipped
+// is c + 8; as the low bits of 1024 it reads 1032 + c, four bits up 1024 + 16 (c + 8)
+__device__ __forceinline__ uint4 widen8_pairs(uint32_t w)
+{
+    const __half2 k1032 = __float2half2_rn(1032.0f), k16 = __float2half2_rn(0.0625f), k72 = __float2half2_rn(-72.0f);
+    const uint32_t x[4] = {lop_and_xor(w, 0x000f000fu, 0x64086408u), lop_and_xor(w, 0x00f000f0u, 0x64806480u),
+                           lop_and_xor(w >> 8, 0x000f000fu, 0x64086408u),
+                           lop_and_xor(w >> 8, 0x00f000f0u, 0x64806480u)};
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const __half2 h = *reinterpret_cast<const __half2 *>(&x[i]);
+        r[i] = h2_bits(i & 1 ? __hfma2(h, k16, k72) : __hsub2(h, k1032));
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// the order widen8_pairs gives, for 8 elements of a query row
+__device__ __forceinline__ uint4 as_pairs(uint4 v)
+{
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.y, v.w, 0x7632));
+}
+
+}  // namespace
+
+template <int FMT>
+__global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeightsParams p)
+{
+    constexpr int RB = FMT == KVQ_INT4_B64 ? 64 : 128;
+    constexpr uint32_t kPageBytes = kPage * RB;
+    extern __shared__ __align__(1024) uint8_t smem_win[];
+    WinSmem &sm = *reinterpret_cast<WinSmem *>(smem_win);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int H = p.num_heads, G = p.group;
+    pdl_launch_dependents();
+    if (tid == 0) {
+        for (int i = 0; i < kCodeStages; i++) {
+            mbar_init(&sm.code_full[i], 1);
+            mbar_init(&sm.code_free[i], 4);
+        }
+        for (int i = 0; i < kKeyStages; i++) {
+            mbar_init(&sm.k_full[i], 4);
+            mbar_init(&sm.k_free[i], 1);
+        }
+        for (int i = 0; i < kScoreStages; i++) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], 4);
+        }
+        mbar_init(&sm.q_free[0], 1);
+        mbar_init(&sm.q_free[1], 1);
+        mbar_init(&sm.mma_done, 1);
+        mbar_init_fence();
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)),
+                     "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    // steps of sequence b: (cache head, tile of query rows, page pair), the pages fastest
+    auto steps_of = [&](const PwSeq &s) { return (s.L + kWinKeys - 1) / kWinKeys; };
+    auto tiles_of = [&](const PwSeq &s) { return (s.n * G + kWinRows - 1) / kWinRows; };
+    if (warp == 13) {
+        int64_t run = 0;
+        for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+            int64_t u = 0;
+            if (b0 + lane < p.num_seqs) {
+                PwSeq s;
+                if (pw_seq(p, b0 + lane, s))
+                    u = (int64_t)steps_of(s) * H * tiles_of(s);
+                else if (blockIdx.x == 0)
+                    set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(kFull, u, o);
+                if (lane >= o) u += v;
+            }
+            if (b0 + lane < p.num_seqs) sm.upto[b0 + lane + 1] = run + u;
+            run += __shfl_sync(kFull, u, 31);
+        }
+        if (lane == 0) sm.upto[0] = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const int64_t U = sm.upto[p.num_seqs];
+    const int64_t first = U * blockIdx.x / gridDim.x;
+    const int steps = (int)(U * (blockIdx.x + 1) / gridDim.x - first);
+    bool ok = true;
+
+    if (warp < 4) {
+        // ---- widening ----
+        const __half2 flip = __float2half2_rn(p.score_scale < 0.0f ? -1.0f : 1.0f);
+        int tiles = 0;  // query tiles staged so far
+        for (int i = 0; i < steps; i++) {
+            const int cs = i % kCodeStages, ks = i % kKeyStages;
+            ok = mbar_wait_bounded(&sm.code_full[cs], (uint32_t)(i / kCodeStages) & 1u);
+            const WinStep m = sm.meta[i % kMeta];
+            if (ok && m.first) {
+                if (tiles >= 2) ok = mbar_wait_bounded(&sm.q_free[m.qbuf], (uint32_t)(tiles / 2 - 1) & 1u);
+                tiles++;
+            }
+            if (ok && i >= kKeyStages) ok = mbar_wait_bounded(&sm.k_free[ks], (uint32_t)(i / kKeyStages - 1) & 1u);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            if (m.first) {
+                const int rows = m.n * G;
+#pragma unroll 4
+                for (int e = tid; e < kWinRows * 16; e += 128) {
+                    const int r = e >> 4, c = e & 15, rr = m.row0 + r;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (rr < rows) {
+                        v = *reinterpret_cast<const uint4 *>(
+                            p.q + ((int64_t)(m.c0 + rr / G) * p.num_q_heads + m.h * G + rr % G) * kHeadDim + 8 * c);
+                        uint32_t *x = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                        for (int y = 0; y < 4; y++) x[y] = h2_bits(__hmul2(*reinterpret_cast<__half2 *>(&x[y]), flip));
+                    }
+                    *reinterpret_cast<uint4 *>(sm.q[m.qbuf] + tile_chunk(r, c)) = FMT == KVQ_INT4_B64 ? as_pairs(v) : v;
+                }
+            }
+            const uint8_t *src = sm.code[cs];
+            uint8_t *dst = sm.k[ks];
+            constexpr int kLd = 2 * kPageBytes / (16 * 128);  // 16-byte pieces per thread
+#pragma unroll
+            for (int r = 0; r < kLd; r++) {
+                if constexpr (FMT == KVQ_INT4_B64) {  // 8 threads: 4 keys x 2 pieces (both sides free of conflicts)
+                    const int key = (r >> 1) * kPage + 4 * (tid >> 3) + ((tid & 7) >> 1), pc = (tid & 1) + 2 * (r & 1);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + key * RB + 16 * pc);
+                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc)) = widen8_pairs(w.x);
+                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc + 1)) = widen8_pairs(w.y);
+                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc + 2)) = widen8_pairs(w.z);
+                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc + 3)) = widen8_pairs(w.w);
+                } else {  // 8 threads: 2 keys x 4 pieces
+                    const int key = 32 * (r >> 1) + 2 * (tid >> 3) + ((tid & 7) >> 2), pc = (tid & 3) + 4 * (r & 1);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + key * RB + 16 * pc);
+                    const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        __half2 a[2], b[2];
+                        widen_bytes<FMT>(wd[2 * x], a);
+                        widen_bytes<FMT>(wd[2 * x + 1], b);
+                        *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 2 * pc + x)) =
+                            make_uint4(h2_bits(a[0]), h2_bits(a[1]), h2_bits(b[0]), h2_bits(b[1]));
+                    }
+                }
+            }
+            fence_proxy_async_smem();  // the MMAs read through the async proxy
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm.k_full[ks]);
+                mbar_arrive(&sm.code_free[cs]);
+            }
+        }
+    } else if (warp < 12) {
+        // ---- softmax sums: one query row per thread ----
+        const int row = (warp & 3) * 32 + lane;
+        const float sabs = fmaxf(fabsf(p.score_scale), kPwMinScale);
+        for (int i = (warp - 4) >> 2; i < steps; i += 2) {
+            const int ss = i % kScoreStages;
+            ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[ss], (uint32_t)(i / kScoreStages) & 1u));
+            if (!ok) break;
+            tc_fence_after();
+            const WinStep m = sm.meta[i % kMeta];
+            const uint32_t tm = tmem + 128u * ss + ((uint32_t)((warp & 3) * 32) << 16);
+            const int rr = m.row0 + row, pos0 = m.L - m.n, pos = pos0 + rr / G;
+            float *dst = p.lse + ((int64_t)(m.c0 + rr / G) * p.num_q_heads + m.h * G + rr % G) * p.max_blocks + m.j;
+#pragma unroll
+            for (int hh = 0; hh < 2; hh++) {
+                uint32_t x[2][32];
+                tmem_ld32_async(tm + 64 * hh, x[0]);
+                tmem_ld32_async(tm + 64 * hh + 32, x[1]);
+                tmem_ld_wait();
+                if (hh == 1) {  // S may be written again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.s_free[ss]);
+                }
+                float s[64];
+#pragma unroll
+                for (int e = 0; e < 64; e++) s[e] = __uint_as_float(x[e >> 5][e & 31]);
+                const int k0 = (m.j + hh) * kPage;
+                if (k0 + kPage - 1 > pos0) {  // keys past some row's position
+#pragma unroll
+                    for (int e = 0; e < 64; e++)
+                        if (k0 + e > pos) s[e] = -INFINITY;
+                }
+                float m8[8];
+#pragma unroll
+                for (int y = 0; y < 8; y++) {
+                    const float *v = s + 8 * y;
+                    m8[y] = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
+                }
+                const float mx = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+                const float f = fmaxf(m.sk[hh] * sabs, kPwMinScale);
+                const float off = mx == -INFINITY ? 0.0f : -f * mx;
+                const uint64_t f2 = pk2(f, f), r2 = pk2(off, off);
+                uint64_t sum[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 32; e++) {
+                    float x0, x1;
+                    upk2(fma2(pk2(s[2 * e], s[2 * e + 1]), f2, r2), x0, x1);
+                    sum[e & 3] = add2(sum[e & 3], pk2(ex2_approx(x0), ex2_approx(x1)));
+                }
+                float la, lb;
+                upk2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), la, lb);
+                if (hh < m.pages && rr < m.n * G) dst[hh] = f * mx + __log2f(la + lb);
+            }
+        }
+    } else if (warp == 12) {
+        if (lane == 0) {
+            // ---- the MMA thread ----
+            const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.q[0])) >> 32);
+            const uint32_t q_lo = (uint32_t)umma_desc(smem_addr(sm.q[0])), k_lo = (uint32_t)umma_desc(smem_addr(sm.k[0]));
+            for (int i = 0; i < steps && ok; i++) {
+                const int ks = i % kKeyStages, ss = i % kScoreStages;
+                ok = mbar_wait_bounded(&sm.k_full[ks], (uint32_t)(i / kKeyStages) & 1u);
+                if (ok && i >= kScoreStages)
+                    ok = mbar_wait_bounded(&sm.s_free[ss], (uint32_t)(i / kScoreStages - 1) & 1u);
+                if (!ok) break;
+                tc_fence_after();
+                const int qbuf = sm.meta[i % kMeta].qbuf, last = sm.meta[i % kMeta].last;
+                const uint32_t a = q_lo + qbuf * (kWinTile >> 4), b = k_lo + ks * (kWinTile >> 4);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const uint32_t d = (uint32_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
+                    umma_f16_ss(tmem + 128 * ss, a + d, hi, b + d, hi, kWinIdesc, k > 0 ? 1u : 0u);
+                }
+                umma_commit(&sm.s_full[ss]);
+                umma_commit(&sm.k_free[ks]);
+                if (last) umma_commit(&sm.q_free[qbuf]);
+            }
+            umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
+            if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
+        }
+    } else {
+        // ---- pages and copies: lane l looks up step l of 32, two rings in turn ----
+        WinStep ring[2];
+        uint32_t ph[2][2];
+        auto look = [&](int i, WinStep &m, uint32_t (&at)[2]) {
+            if (i + lane >= steps) return;
+            const int64_t u = first + i + lane;
+            int lo = 0, hi = p.num_seqs;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (sm.upto[mid] <= u)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            PwSeq s;
+            pw_seq(p, lo, s);
+            const int np = (s.L + kPage - 1) / kPage, nst = steps_of(s), tiles = tiles_of(s);
+            const int64_t r = u - sm.upto[lo], hr = r / nst;
+            const int k = (int)(r - hr * nst);
+            m.c0 = s.c0;
+            m.n = s.n;
+            m.L = s.L;
+            m.h = (int)(hr / tiles);
+            m.row0 = (int)(hr % tiles) * kWinRows;
+            m.j = 2 * k;
+            m.pages = min(2, np - m.j);
+            m.first = k == 0 || i + lane == 0;
+            m.last = k == nst - 1 || i + lane == steps - 1;
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                at[x] = 0;
+                m.sk[x] = 0.0f;
+                if (x >= m.pages) continue;
+                int pg = p.block_table[(int64_t)lo * p.max_blocks + m.j + x];
+                if (pg < 0 || pg >= p.num_pages) {
+                    set_flag(p.status, KVQ_FLAG_BAD_PAGE);
+                    pg = 0;
+                }
+                at[x] = (uint32_t)pg * (uint32_t)H + (uint32_t)m.h;
+                m.sk[x] = p.k_scales[at[x]];
+            }
+        };
+        look(0, ring[0], ph[0]);
+        look(32, ring[1], ph[1]);
+        int qbuf = 1, used = 0;
+        for (int i = 0; i < steps; i++) {
+            if (i > 0 && (i & 31) == 0) {
+                if (i & 32)
+                    look(i + 32, ring[0], ph[0]);
+                else
+                    look(i + 32, ring[1], ph[1]);
+            }
+            const int cs = i % kCodeStages;
+            if (i >= kCodeStages)
+                ok = __all_sync(kFull, mbar_wait_bounded(&sm.code_free[cs], (uint32_t)(i / kCodeStages - 1) & 1u));
+            if (!ok) break;
+            auto issue = [&](WinStep &m, const uint32_t (&at)[2]) {
+                qbuf ^= __shfl_sync(kFull, m.first, i & 31);
+                if (lane == (i & 31)) {
+                    m.qbuf = qbuf;
+                    sm.meta[i % kMeta] = m;
+                    mbar_arrive_expect_tx(&sm.code_full[cs], m.pages * kPageBytes);
+                    for (int x = 0; x < m.pages; x++)
+                        bulk_copy_g2s(sm.code[cs] + x * kPageBytes, p.k_codes + (size_t)at[x] * kPageBytes, kPageBytes,
+                                      &sm.code_full[cs]);
+                }
+            };
+            if (i & 32)
+                issue(ring[1], ph[1]);
+            else
+                issue(ring[0], ph[0]);
+            used = i + 1;
+        }
+        // no copy in flight when the CTA ends
+        for (int i = max(0, used - kCodeStages); i < used; i++)
+            if (!mbar_wait_bounded(&sm.code_full[i % kCodeStages], (uint32_t)(i / kCodeStages) & 1u)) ok = false;
+    }
+    __syncwarp();
+    if (!ok) set_flag(p.status, KVQ_FLAG_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+}
+
+template <int FMT>
+static cudaError_t launch_page_window_fmt(const PageWeightsParams &p, int num_sms, cudaStream_t s)
+{
+    cudaError_t e = cudaFuncSetAttribute(page_window_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(WinSmem));
+    if (e != cudaSuccess) return e;
+    return launch_plain(page_window_kernel<FMT>, dim3((unsigned)num_sms), dim3(kWinThreads), sizeof(WinSmem), s, p);
+}
+
+cudaError_t launch_page_window(int fmt, const PageWeightsParams &p, int num_sms, cudaStream_t s)
+{
+    if (fmt == KVQ_INT4_B64) return launch_page_window_fmt<KVQ_INT4_B64>(p, num_sms, s);
+    if (fmt == KVQ_FP8_E4M3) return launch_page_window_fmt<KVQ_FP8_E4M3>(p, num_sms, s);
+    return launch_page_window_fmt<KVQ_INT8_PAGE>(p, num_sms, s);
+}
+
+}  // namespace kvq
