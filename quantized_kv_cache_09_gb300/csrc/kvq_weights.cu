@@ -176,7 +176,6 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
         pj_ = x.j;
     };
     look(0, ph[0], sk[0], pj[0]);
-    look(32, ph[1], sk[1], pj[1]);
     const int chunks = units * F::kChunks;
     uint8_t *ring = sm.ring[warp][0];
     uint64_t *full = sm.full[warp];
@@ -195,6 +194,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     };
     __syncwarp();
     for (int c = 0; c < kPwStages; c++) bring(c);
+    look(32, ph[1], sk[1], pj[1]);
 
     uint32_t qb[NT][8][2];       // the unit's query rows as the B operand: column g of tile nt is row row0 + 8 nt + g
     float bias[NT][2];           // columns 2t, 2t + 1: minus the offset share of every raw score (int4)
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
 // Rows [64 c, 64 c + 64) of sequence b (query rows, tokens x heads): the rows' log2-sums over
 // the pages (one pass: maximum and sum together), then each page's mass over these rows, to the
 // output (one chunk) or to `part`.
-__global__ void __launch_bounds__(kSumThreads) page_sum_kernel(PageWeightsParams p)
+__global__ void __launch_bounds__(kSumThreads, 2) page_sum_kernel(PageWeightsParams p)
 {
     constexpr int kGroups = 4, kTile = kSumThreads / kGroups;  // a tile of pages x groups of rows
     __shared__ float total[kPwSumRows];

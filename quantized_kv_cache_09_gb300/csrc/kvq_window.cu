@@ -22,35 +22,48 @@ namespace kvq {
 
 namespace {
 
-constexpr int kWinThreads = 14 * 32;
+constexpr int kWinThreads = 18 * 32;
 constexpr int kWinRows = 128;
 constexpr int kWinKeys = 2 * kPage;
-constexpr int kCodeStages = 5, kKeyStages = 2, kScoreStages = 4, kMeta = 16;
+constexpr int kCodeStages = 5, kKeyStages = 4, kScoreStages = 3, kMeta = 16;
 // a step's record lives until its sums are done: the copies run at most the sum of the stages ahead
 static_assert(kMeta >= kCodeStages + kKeyStages + kScoreStages + 2, "records outlive their steps");
-constexpr int kWinTile = kWinRows * kHeadDim * 2;
+constexpr int kWinTile = kWinKeys * kHeadDim * 2;
+constexpr uint32_t kWinTmem = 512;    // S at columns 128 * stage, Q at 384 + 64 * buffer
 constexpr uint32_t kWinIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);  // f32 += f16 x f16, M = N = 128
 
 // what a step is: its sequence, cache head, first query row and page, key scales of its pages
 struct WinStep {
-    int32_t c0, n, L, h, row0, j, pages, qbuf;
-    float sk[2];
+    int32_t c0, n, L, h, row0, j, pages;
     int32_t first, last;  // of its tile's run in this CTA
+    float sk[2];
 };
 
 struct alignas(1024) WinSmem {
-    uint8_t q[2][kWinTile];
     uint8_t k[kKeyStages][kWinTile];
     uint8_t code[kCodeStages][2 * kPage * kHeadDim];
     uint64_t code_full[kCodeStages], code_free[kCodeStages];
     uint64_t k_full[kKeyStages], k_free[kKeyStages];
     uint64_t s_full[kScoreStages], s_free[kScoreStages];
-    uint64_t q_free[2], mma_done;
+    uint64_t q_full[2], q_free[2], mma_done;
     WinStep meta[kMeta];
     int64_t upto[kMaxSeqsPerLaunch + 1];
     uint32_t tmem;
 };
 static_assert(sizeof(WinSmem) <= 227 * 1024, "one CTA's shared memory");
+
+// counter i of a ring of N stages: its stage and the parity of its use
+template <int N>
+struct Turn {
+    uint32_t stage = 0, parity = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++stage == N) {
+            stage = 0;
+            parity ^= 1u;
+        }
+    }
+};
 
 // byte offset of elements 8c .. 8c + 7 of row r in a K-major tile of 128 rows, 128-byte swizzled
 __device__ __forceinline__ uint32_t tile_chunk(int r, int c)
@@ -114,14 +127,16 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             mbar_init(&sm.s_full[i], 1);
             mbar_init(&sm.s_free[i], 4);
         }
-        mbar_init(&sm.q_free[0], 1);
-        mbar_init(&sm.q_free[1], 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sm.q_full[i], 4);
+            mbar_init(&sm.q_free[i], 1);
+        }
         mbar_init(&sm.mma_done, 1);
         mbar_init_fence();
     }
     if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)),
-                     "r"(512u));
+                     "r"(kWinTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     // steps of sequence b: (cache head, tile of query rows, page pair), the pages fastest
@@ -152,6 +167,32 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
+    // step u of the launch: its sequence; of it the step's record, but for the scales and flags; and
+    // its number among the tile's `all` steps
+    auto place = [&](int64_t u, WinStep &m, int &k, int &all) {
+        int lo = 0, hi = p.num_seqs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sm.upto[mid] <= u)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        PwSeq s;
+        pw_seq(p, lo, s);
+        all = steps_of(s);
+        const int tiles = tiles_of(s);
+        const int64_t r = u - sm.upto[lo], hr = r / all;
+        k = (int)(r - hr * all);
+        m.c0 = s.c0;
+        m.n = s.n;
+        m.L = s.L;
+        m.h = (int)(hr / tiles);
+        m.row0 = (int)(hr % tiles) * kWinRows;
+        m.j = 2 * k;
+        m.pages = min(2, (s.L + kPage - 1) / kPage - m.j);
+        return lo;
+    };
     const int64_t U = sm.upto[p.num_seqs];
     const int64_t first = U * blockIdx.x / gridDim.x;
     const int steps = (int)(U * (blockIdx.x + 1) / gridDim.x - first);
@@ -159,75 +200,60 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
 
     if (warp < 4) {
         // ---- widening ----
-        const __half2 flip = __float2half2_rn(p.score_scale < 0.0f ? -1.0f : 1.0f);
-        int tiles = 0;  // query tiles staged so far
-        for (int i = 0; i < steps; i++) {
-            const int cs = i % kCodeStages, ks = i % kKeyStages;
-            ok = mbar_wait_bounded(&sm.code_full[cs], (uint32_t)(i / kCodeStages) & 1u);
-            const WinStep m = sm.meta[i % kMeta];
-            if (ok && m.first) {
-                if (tiles >= 2) ok = mbar_wait_bounded(&sm.q_free[m.qbuf], (uint32_t)(tiles / 2 - 1) & 1u);
-                tiles++;
-            }
-            if (ok && i >= kKeyStages) ok = mbar_wait_bounded(&sm.k_free[ks], (uint32_t)(i / kKeyStages - 1) & 1u);
+        Turn<kCodeStages> code;
+        Turn<kKeyStages> key;
+        for (int i = 0; i < steps; i++, code.next(), key.next()) {
+            ok = mbar_wait_bounded(&sm.code_full[code.stage], code.parity);
+            constexpr int kLd = 2 * kPageBytes / (16 * 128);  // 16-byte pieces per thread
+            // int4: 8 threads take 4 keys x 2 pieces (16 bytes of a row), else 2 keys x 4 pieces: the
+            // stores meet no bank conflict
+            auto key_of = [&](int r) {
+                return RB == 64 ? (r >> 1) * kPage + 4 * (tid >> 3) + ((tid & 7) >> 1)
+                                : 32 * (r >> 1) + 2 * (tid >> 3) + ((tid & 7) >> 2);
+            };
+            auto piece_of = [&](int r) { return RB == 64 ? (tid & 1) + 2 * (r & 1) : (tid & 3) + 4 * (r & 1); };
+            uint4 w[kLd];
+#pragma unroll
+            for (int r = 0; r < kLd; r++) w[r] = *reinterpret_cast<const uint4 *>(sm.code[code.stage] + key_of(r) * RB + 16 * piece_of(r));
+            if (ok && i >= kKeyStages) ok = mbar_wait_bounded(&sm.k_free[key.stage], key.parity ^ 1u);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
-            if (m.first) {
-                const int rows = m.n * G;
-#pragma unroll 4
-                for (int e = tid; e < kWinRows * 16; e += 128) {
-                    const int r = e >> 4, c = e & 15, rr = m.row0 + r;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (rr < rows) {
-                        v = *reinterpret_cast<const uint4 *>(
-                            p.q + ((int64_t)(m.c0 + rr / G) * p.num_q_heads + m.h * G + rr % G) * kHeadDim + 8 * c);
-                        uint32_t *x = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                        for (int y = 0; y < 4; y++) x[y] = h2_bits(__hmul2(*reinterpret_cast<__half2 *>(&x[y]), flip));
-                    }
-                    *reinterpret_cast<uint4 *>(sm.q[m.qbuf] + tile_chunk(r, c)) = FMT == KVQ_INT4_B64 ? as_pairs(v) : v;
-                }
-            }
-            const uint8_t *src = sm.code[cs];
-            uint8_t *dst = sm.k[ks];
-            constexpr int kLd = 2 * kPageBytes / (16 * 128);  // 16-byte pieces per thread
+            uint8_t *dst = sm.k[key.stage];
 #pragma unroll
             for (int r = 0; r < kLd; r++) {
-                if constexpr (FMT == KVQ_INT4_B64) {  // 8 threads: 4 keys x 2 pieces (both sides free of conflicts)
-                    const int key = (r >> 1) * kPage + 4 * (tid >> 3) + ((tid & 7) >> 1), pc = (tid & 1) + 2 * (r & 1);
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + key * RB + 16 * pc);
-                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc)) = widen8_pairs(w.x);
-                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc + 1)) = widen8_pairs(w.y);
-                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc + 2)) = widen8_pairs(w.z);
-                    *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 4 * pc + 3)) = widen8_pairs(w.w);
-                } else {  // 8 threads: 2 keys x 4 pieces
-                    const int key = 32 * (r >> 1) + 2 * (tid >> 3) + ((tid & 7) >> 2), pc = (tid & 3) + 4 * (r & 1);
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + key * RB + 16 * pc);
-                    const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+                const int kk = key_of(r), pc = piece_of(r);
+                const uint32_t x[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+                if constexpr (FMT == KVQ_INT4_B64) {
 #pragma unroll
-                    for (int x = 0; x < 2; x++) {
+                    for (int y = 0; y < 4; y++)
+                        *reinterpret_cast<uint4 *>(dst + tile_chunk(kk, 4 * pc + y)) = widen8_pairs(x[y]);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 2; y++) {
                         __half2 a[2], b[2];
-                        widen_bytes<FMT>(wd[2 * x], a);
-                        widen_bytes<FMT>(wd[2 * x + 1], b);
-                        *reinterpret_cast<uint4 *>(dst + tile_chunk(key, 2 * pc + x)) =
+                        widen_bytes<FMT>(x[2 * y], a);
+                        widen_bytes<FMT>(x[2 * y + 1], b);
+                        *reinterpret_cast<uint4 *>(dst + tile_chunk(kk, 2 * pc + y)) =
                             make_uint4(h2_bits(a[0]), h2_bits(a[1]), h2_bits(b[0]), h2_bits(b[1]));
                     }
                 }
             }
-            fence_proxy_async_smem();  // the MMAs read through the async proxy
+            fence_proxy_async_smem();  // the MMAs read through the async proxy, the next copy writes through it
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sm.k_full[ks]);
-                mbar_arrive(&sm.code_free[cs]);
+                mbar_arrive(&sm.k_full[key.stage]);
+                mbar_arrive(&sm.code_free[code.stage]);
             }
         }
     } else if (warp < 12) {
         // ---- softmax sums: one query row per thread ----
         const int row = (warp & 3) * 32 + lane;
         const float sabs = fmaxf(fabsf(p.score_scale), kPwMinScale);
-        for (int i = (warp - 4) >> 2; i < steps; i += 2) {
-            const int ss = i % kScoreStages;
-            ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[ss], (uint32_t)(i / kScoreStages) & 1u));
+        Turn<kScoreStages> score;
+        for (int i = 0; i < steps; i++, score.next()) {
+            if ((i & 1) != (warp - 4) >> 2) continue;
+            const uint32_t ss = score.stage;
+            ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[ss], score.parity));
             if (!ok) break;
             tc_fence_after();
             const WinStep m = sm.meta[i % kMeta];
@@ -279,64 +305,49 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     } else if (warp == 12) {
         if (lane == 0) {
             // ---- the MMA thread ----
-            const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.q[0])) >> 32);
-            const uint32_t q_lo = (uint32_t)umma_desc(smem_addr(sm.q[0])), k_lo = (uint32_t)umma_desc(smem_addr(sm.k[0]));
-            for (int i = 0; i < steps && ok; i++) {
-                const int ks = i % kKeyStages, ss = i % kScoreStages;
-                ok = mbar_wait_bounded(&sm.k_full[ks], (uint32_t)(i / kKeyStages) & 1u);
-                if (ok && i >= kScoreStages)
-                    ok = mbar_wait_bounded(&sm.s_free[ss], (uint32_t)(i / kScoreStages - 1) & 1u);
+            const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.k[0])) >> 32);
+            const uint32_t k_lo = (uint32_t)umma_desc(smem_addr(sm.k[0]));
+            Turn<kKeyStages> key;
+            Turn<kScoreStages> score;
+            Turn<2> query;
+            for (int i = 0; i < steps && ok; i++, key.next(), score.next()) {
+                ok = mbar_wait_bounded(&sm.k_full[key.stage], key.parity);
+                if (ok && sm.meta[i % kMeta].first) ok = mbar_wait_bounded(&sm.q_full[query.stage], query.parity);
+                if (ok && i >= kScoreStages) ok = mbar_wait_bounded(&sm.s_free[score.stage], score.parity ^ 1u);
                 if (!ok) break;
                 tc_fence_after();
-                const int qbuf = sm.meta[i % kMeta].qbuf, last = sm.meta[i % kMeta].last;
-                const uint32_t a = q_lo + qbuf * (kWinTile >> 4), b = k_lo + ks * (kWinTile >> 4);
+                const uint32_t b = k_lo + key.stage * (kWinTile >> 4), a = tmem + 384 + 64 * query.stage;
 #pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    const uint32_t d = (uint32_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
-                    umma_f16_ss(tmem + 128 * ss, a + d, hi, b + d, hi, kWinIdesc, k > 0 ? 1u : 0u);
+                for (int k = 0; k < 8; k++)
+                    umma_f16_ts(tmem + 128 * score.stage, a + 8 * k,
+                                b + (uint32_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), hi, kWinIdesc,
+                                k > 0 ? 1u : 0u);
+                umma_commit(&sm.s_full[score.stage]);
+                umma_commit(&sm.k_free[key.stage]);
+                if (sm.meta[i % kMeta].last) {
+                    umma_commit(&sm.q_free[query.stage]);
+                    query.next();
                 }
-                umma_commit(&sm.s_full[ss]);
-                umma_commit(&sm.k_free[ks]);
-                if (last) umma_commit(&sm.q_free[qbuf]);
             }
             umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
             if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
         }
-    } else {
+    } else if (warp == 13) {
         // ---- pages and copies: lane l looks up step l of 32, two rings in turn ----
         WinStep ring[2];
         uint32_t ph[2][2];
         auto look = [&](int i, WinStep &m, uint32_t (&at)[2]) {
             if (i + lane >= steps) return;
-            const int64_t u = first + i + lane;
-            int lo = 0, hi = p.num_seqs;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (sm.upto[mid] <= u)
-                    lo = mid;
-                else
-                    hi = mid;
-            }
-            PwSeq s;
-            pw_seq(p, lo, s);
-            const int np = (s.L + kPage - 1) / kPage, nst = steps_of(s), tiles = tiles_of(s);
-            const int64_t r = u - sm.upto[lo], hr = r / nst;
-            const int k = (int)(r - hr * nst);
-            m.c0 = s.c0;
-            m.n = s.n;
-            m.L = s.L;
-            m.h = (int)(hr / tiles);
-            m.row0 = (int)(hr % tiles) * kWinRows;
-            m.j = 2 * k;
-            m.pages = min(2, np - m.j);
+            int k, all;
+            const int b = place(first + i + lane, m, k, all);
             m.first = k == 0 || i + lane == 0;
-            m.last = k == nst - 1 || i + lane == steps - 1;
+            m.last = k == all - 1 || i + lane == steps - 1;
 #pragma unroll
             for (int x = 0; x < 2; x++) {
                 at[x] = 0;
                 m.sk[x] = 0.0f;
                 if (x >= m.pages) continue;
-                int pg = p.block_table[(int64_t)lo * p.max_blocks + m.j + x];
+                int pg = p.block_table[(int64_t)b * p.max_blocks + m.j + x];
                 if (pg < 0 || pg >= p.num_pages) {
                     set_flag(p.status, KVQ_FLAG_BAD_PAGE);
                     pg = 0;
@@ -347,27 +358,25 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
         };
         look(0, ring[0], ph[0]);
         look(32, ring[1], ph[1]);
-        int qbuf = 1, used = 0;
-        for (int i = 0; i < steps; i++) {
+        Turn<kCodeStages> code;
+        int used = 0;
+        for (int i = 0; i < steps; i++, code.next()) {
             if (i > 0 && (i & 31) == 0) {
                 if (i & 32)
                     look(i + 32, ring[0], ph[0]);
                 else
                     look(i + 32, ring[1], ph[1]);
             }
-            const int cs = i % kCodeStages;
-            if (i >= kCodeStages)
-                ok = __all_sync(kFull, mbar_wait_bounded(&sm.code_free[cs], (uint32_t)(i / kCodeStages - 1) & 1u));
+            if (i >= kCodeStages) ok = __all_sync(kFull, mbar_wait_bounded(&sm.code_free[code.stage], code.parity ^ 1u));
             if (!ok) break;
-            auto issue = [&](WinStep &m, const uint32_t (&at)[2]) {
-                qbuf ^= __shfl_sync(kFull, m.first, i & 31);
+            auto issue = [&](const WinStep &m, const uint32_t (&at)[2]) {
                 if (lane == (i & 31)) {
-                    m.qbuf = qbuf;
                     sm.meta[i % kMeta] = m;
-                    mbar_arrive_expect_tx(&sm.code_full[cs], m.pages * kPageBytes);
+                    uint64_t *bar = &sm.code_full[code.stage];
+                    mbar_arrive_expect_tx(bar, m.pages * kPageBytes);
                     for (int x = 0; x < m.pages; x++)
-                        bulk_copy_g2s(sm.code[cs] + x * kPageBytes, p.k_codes + (size_t)at[x] * kPageBytes, kPageBytes,
-                                      &sm.code_full[cs]);
+                        bulk_copy_g2s(sm.code[code.stage] + x * kPageBytes, p.k_codes + (size_t)at[x] * kPageBytes,
+                                      kPageBytes, bar);
                 }
             };
             if (i & 32)
@@ -379,13 +388,50 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
         // no copy in flight when the CTA ends
         for (int i = max(0, used - kCodeStages); i < used; i++)
             if (!mbar_wait_bounded(&sm.code_full[i % kCodeStages], (uint32_t)(i / kCodeStages) & 1u)) ok = false;
+    } else {
+        // ---- query rows ----
+        const int row = (warp & 3) * 32 + lane;
+        const __half2 flip = __float2half2_rn(p.score_scale < 0.0f ? -1.0f : 1.0f);
+        Turn<2> query;
+        int tiles = 0;
+        for (int i = 0; i < steps; tiles++, query.next()) {
+            WinStep m;
+            int k, all;
+            place(first + i, m, k, all);
+            i += all - k;
+            const int rr = m.row0 + row;
+            const bool live = rr < m.n * G;
+            const uint4 *q = reinterpret_cast<const uint4 *>(
+                p.q + ((int64_t)(m.c0 + rr / G) * p.num_q_heads + m.h * G + rr % G) * kHeadDim);
+            uint32_t x[2][32];
+#pragma unroll
+            for (int c = 0; c < 16; c++) {
+                uint4 v = live ? q[c] : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (FMT == KVQ_INT4_B64) v = as_pairs(v);
+                const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    x[c >> 3][4 * (c & 7) + e] = h2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&y[e]), flip));
+            }
+            if (tiles >= 2) ok = mbar_wait_bounded(&sm.q_free[query.stage], query.parity ^ 1u);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tm = tmem + 384 + 64 * query.stage + ((uint32_t)((warp & 3) * 32) << 16);
+            tmem_st32(tm, x[0]);
+            tmem_st32(tm + 32, x[1]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_full[query.stage]);
+        }
     }
     __syncwarp();
     if (!ok) set_flag(p.status, KVQ_FLAG_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     if (warp == 12)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kWinTmem));
 }
 
 template <int FMT>
