@@ -9,6 +9,7 @@ entry point that launches work is wrapped in an NVTX range named after its C
 function, for profilers that filter by range (ncu --nvtx --nvtx-include ...);
 unset, the wrappers are the plain functions.
 """
+import contextlib
 import ctypes
 import functools
 import os
@@ -161,13 +162,34 @@ def lib():
     return _lib
 
 
+_current_device = torch.cuda.current_device
+
+
+def _on(index):
+    """A context with device `index` current: none where it already is (entering one costs more than a launch's
+    other host work)."""
+    return _NOTHING if index == _current_device() else torch.cuda.device(index)
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _dense(index, dtype, **tensors):
+    """Refuse what is no contiguous tensor of dtype on CUDA device `index`."""
+    for name, t in tensors.items():
+        if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index or index < 0:
+            _cuda(t, dtype, name)
+            raise ValueError(f"{name} is on another device")
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
 def _stream(stream, device=None):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        index = None if device is None else torch.device(device).index
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(_current_device() if index is None else index))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -336,13 +358,14 @@ def kvq_prefill_attention(cache, q, cu_seqlens_q, max_q_per_seq, block_table, se
                                        _stream(stream, q.device)), "kvq_prefill_attention")
 
 
-def _rows(t, dtype, name):
-    """The row stride of a CUDA tensor [rows][heads][128] whose rows have no gaps of their own."""
-    if not (t.is_cuda and t.dim() == 3 and t.dtype == dtype and t.shape[2] == HEAD_DIM):
-        raise ValueError(f"{name} must be a CUDA {dtype} tensor [rows][heads][{HEAD_DIM}]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != HEAD_DIM):
+def _rows(t, dtype, index, name):
+    """The row stride of a tensor [rows][heads][128] on CUDA device `index`, whose rows have no gaps of their own."""
+    if t.dtype is not dtype or t.dim() != 3 or t.shape[2] != HEAD_DIM or t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor [rows][heads][{HEAD_DIM}], on q's device")
+    row, head, element = t.stride()
+    if element != 1 or (head != HEAD_DIM and t.shape[1] > 1):
         raise ValueError(f"{name}: the heads of a row must lie side by side")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
+    return row if t.shape[0] > 1 else t.shape[1] * HEAD_DIM
 
 
 @_nvtx
@@ -354,27 +377,29 @@ def kvq_prompt_attention(q, k, v, cu_seqlens, max_tokens_per_seq, softmax_scale,
     and v may be views with gaps between rows (slices of one fused projection).
     lse (optional) fp32 [total][Hq]: ln of the softmax's denominator.  status
     (optional) int32[1]: KVQ_FLAG_* bits, e.g. the cache's status word."""
-    if q.dtype not in (torch.float16, torch.bfloat16):
+    dtype = q.dtype
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
         raise ValueError("q must be a CUDA float16 or bfloat16 tensor")
-    strides = [_rows(t, q.dtype, n) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    _cuda(out, q.dtype, "out")
-    _cuda(cu_seqlens, torch.int32, "cu_seqlens")
+    dev = q.get_device()
+    qs, ks, vs = _rows(q, dtype, dev, "q"), _rows(k, dtype, dev, "k"), _rows(v, dtype, dev, "v")
+    _dense(dev, dtype, out=out)
+    _dense(dev, torch.int32, cu_seqlens=cu_seqlens)
     if lse is not None:
-        _cuda(lse, torch.float32, "lse")
+        _dense(dev, torch.float32, lse=lse)
     if status is not None:
-        _cuda(status, torch.int32, "status")
-    T, Hq = q.shape[:2]
-    if (out.shape != q.shape or k.shape != v.shape or k.shape[0] != T or cu_seqlens.dim() != 1 or
-            cu_seqlens.numel() < 1 or (lse is not None and tuple(lse.shape) != (T, Hq)) or
-            (status is not None and status.numel() < 1)):
+        _dense(dev, torch.int32, status=status)
+    T, Hq, _ = q.shape
+    n = cu_seqlens.numel() - 1
+    if (out.shape != q.shape or k.shape != v.shape or k.shape[0] != T or cu_seqlens.dim() != 1 or n < 0 or
+            (lse is not None and lse.shape != (T, Hq)) or (status is not None and status.numel() < 1)):
         raise ValueError("q/k/v/out/lse/cu_seqlens shapes disagree")
-    _one_device(q, k, v, out, cu_seqlens, lse, status)
-    with torch.cuda.device(q.device):
-        _check(lib().kvq_prompt_attention(KVQ_BF16 if q.dtype == torch.bfloat16 else KVQ_FP16, _ptr(q), strides[0],
-                                          _ptr(k), strides[1], _ptr(v), strides[2], Hq, k.shape[1], HEAD_DIM,
-                                          _ptr(cu_seqlens), T, int(max_tokens_per_seq), cu_seqlens.numel() - 1,
-                                          float(softmax_scale), _ptr(out), _ptr(lse), _ptr(status),
-                                          _stream(stream, q.device)), "kvq_prompt_attention")
+    with _on(dev):
+        _check(lib().kvq_prompt_attention(KVQ_BF16 if dtype is torch.bfloat16 else KVQ_FP16, q.data_ptr(), qs,
+                                          k.data_ptr(), ks, v.data_ptr(), vs, Hq, k.shape[1], HEAD_DIM,
+                                          cu_seqlens.data_ptr(), T, int(max_tokens_per_seq), n, float(softmax_scale),
+                                          out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                          None if status is None else status.data_ptr(), _stream(stream, q.device)),
+               "kvq_prompt_attention")
 
 
 def kvq_page_weights_workspace_bytes(total_q, num_q_heads, max_blocks_per_seq):
@@ -395,24 +420,24 @@ def kvq_page_weights(cache, q, cu_seqlens_q, max_q_per_seq, block_table, seq_len
     [total][Hq][128] of its sequence (sequence b's are rows cu[b] .. cu[b+1]-1,
     its last tokens; one row each in a decode step), summed over heads and
     queries.  weights_out may be weights_in."""
-    _cuda(q, torch.float16, "q")
-    for t, n in ((cu_seqlens_q, "cu_seqlens_q"), (block_table, "block_table"), (seq_lens, "seq_lens")):
-        _cuda(t, torch.int32, n)
-    _cuda(weights_out, torch.float32, "weights_out")
+    dev = q.get_device()
+    _dense(dev, torch.float16, q=q)
+    _dense(dev, torch.int32, cu_seqlens_q=cu_seqlens_q, block_table=block_table, seq_lens=seq_lens)
+    _dense(dev, torch.float32, weights_out=weights_out)
     if weights_in is not None:
-        _cuda(weights_in, torch.float32, "weights_in")
-    _cuda(workspace, torch.uint8, "workspace")
+        _dense(dev, torch.float32, weights_in=weights_in)
+    _dense(dev, torch.uint8, workspace=workspace)
     B = seq_lens.numel()
     if (q.dim() != 3 or q.shape[2] != HEAD_DIM or cu_seqlens_q.numel() != B + 1 or block_table.dim() != 2 or
             block_table.shape[0] != B or weights_out.shape != block_table.shape or
             (weights_in is not None and weights_in.shape != block_table.shape)):
         raise ValueError("q/cu_seqlens_q/seq_lens/block_table/weights shapes disagree")
-    _one_device(q, cu_seqlens_q, block_table, seq_lens, weights_in, weights_out, workspace)
-    with torch.cuda.device(q.device):
-        _check(lib().kvq_page_weights(ctypes.byref(cache.struct), _ptr(q), q.shape[1], _ptr(cu_seqlens_q), q.shape[0],
-                                      int(max_q_per_seq), _ptr(block_table), block_table.shape[1], _ptr(seq_lens), B,
-                                      float(softmax_scale), float(decay), _ptr(weights_in), _ptr(weights_out),
-                                      _ptr(workspace), workspace.numel(), _stream(stream, q.device)),
+    with _on(dev):
+        _check(lib().kvq_page_weights(ctypes.byref(cache.struct), q.data_ptr(), q.shape[1], cu_seqlens_q.data_ptr(),
+                                      q.shape[0], int(max_q_per_seq), block_table.data_ptr(), block_table.shape[1],
+                                      seq_lens.data_ptr(), B, float(softmax_scale), float(decay),
+                                      None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(),
+                                      workspace.data_ptr(), workspace.numel(), _stream(stream, q.device)),
                "kvq_page_weights")
 
 
@@ -424,26 +449,25 @@ def kvq_evict_pages(block_table, seq_lens, weights, keep_blocks, sink_blocks, re
     last max(recent_blocks, 1) pages always stay.  table_out: kept pages, then
     the entries past the length, then the num_evicted[b] evicted pages;
     seq_lens_out and weights_out follow.  An output may be its own input."""
-    for t, n in ((block_table, "block_table"), (seq_lens, "seq_lens"), (keep_blocks, "keep_blocks"),
-                 (table_out, "table_out"), (seq_lens_out, "seq_lens_out"), (num_evicted, "num_evicted")):
-        _cuda(t, torch.int32, n)
-    _cuda(weights, torch.float32, "weights")
-    _cuda(weights_out, torch.float32, "weights_out")
+    dev = block_table.get_device()
+    _dense(dev, torch.int32, block_table=block_table, seq_lens=seq_lens, keep_blocks=keep_blocks, table_out=table_out,
+           seq_lens_out=seq_lens_out, num_evicted=num_evicted)
+    _dense(dev, torch.float32, weights=weights, weights_out=weights_out)
     if status is not None:
-        _cuda(status, torch.int32, "status")
+        _dense(dev, torch.int32, status=status)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [num_seqs][max_blocks_per_seq]")
-    B, mb = block_table.shape
-    if (table_out.shape != block_table.shape or weights.shape != block_table.shape or
-            weights_out.shape != block_table.shape or
-            any(t.numel() != B for t in (seq_lens, keep_blocks, seq_lens_out, num_evicted)) or
+    shape = block_table.shape
+    B, mb = shape
+    if (table_out.shape != shape or weights.shape != shape or weights_out.shape != shape or seq_lens.numel() != B or
+            keep_blocks.numel() != B or seq_lens_out.numel() != B or num_evicted.numel() != B or
             (status is not None and status.numel() < 1)):
         raise ValueError("block_table/seq_lens/weights/keep_blocks shapes disagree")
-    _one_device(block_table, seq_lens, weights, keep_blocks, table_out, seq_lens_out, weights_out, num_evicted, status)
-    with torch.cuda.device(block_table.device):
-        _check(lib().kvq_evict_pages(_ptr(block_table), mb, _ptr(seq_lens), _ptr(weights), B, _ptr(keep_blocks),
-                                     int(sink_blocks), int(recent_blocks), _ptr(table_out), _ptr(seq_lens_out),
-                                     _ptr(weights_out), _ptr(num_evicted), _ptr(status),
+    with _on(dev):
+        _check(lib().kvq_evict_pages(block_table.data_ptr(), mb, seq_lens.data_ptr(), weights.data_ptr(), B,
+                                     keep_blocks.data_ptr(), int(sink_blocks), int(recent_blocks),
+                                     table_out.data_ptr(), seq_lens_out.data_ptr(), weights_out.data_ptr(),
+                                     num_evicted.data_ptr(), None if status is None else status.data_ptr(),
                                      _stream(stream, block_table.device)), "kvq_evict_pages")
 
 
