@@ -421,7 +421,7 @@ size_t kvq_page_weights_workspace_bytes(int64_t total_q, int32_t num_q_heads, in
  * Each output may be its input (not another's input or output).  A sequence
  * whose length breaks a bound is copied unchanged, with num_evicted 0, and
  * KVQ_FLAG_BAD_LENGTH set.  Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED
- * (max_blocks_per_seq above 24576: a row is held on one SM), KVQ_ERR_CUDA.
+ * (max_blocks_per_seq above 32768, or more than 2^27 sequences), KVQ_ERR_CUDA.
  */
 kvq_status kvq_evict_pages(const int32_t *block_table, int32_t max_blocks_per_seq, const int32_t *seq_lens,
                            const float *weights, int32_t num_seqs, const int32_t *keep_blocks, int32_t sink_blocks,

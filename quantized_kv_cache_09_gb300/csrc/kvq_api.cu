@@ -373,7 +373,7 @@ kvq_status kvq_evict_pages(const int32_t *block_table, int32_t max_blocks_per_se
                            int32_t *num_evicted, int32_t *status, kvq_stream_t stream)
 {
     if (num_seqs < 0 || max_blocks_per_seq <= 0 || sink_blocks < 0 || recent_blocks < 0) return KVQ_ERR_INVALID_ARG;
-    if (max_blocks_per_seq > kvq::kMaxEvictBlocks) return KVQ_ERR_UNSUPPORTED;
+    if (max_blocks_per_seq > kvq::kMaxEvictBlocks || num_seqs > (1 << 27)) return KVQ_ERR_UNSUPPORTED;
     if (num_seqs == 0) return KVQ_OK;
     if (!block_table || !seq_lens || !weights || !keep_blocks || !table_out || !seq_lens_out || !weights_out ||
         !num_evicted)

@@ -62,8 +62,8 @@ struct EvictParams {
     int num_seqs, max_blocks, sink, recent;
 };
 
-// the longest block-table row an eviction holds on one SM (1.5 million tokens)
-constexpr int kMaxEvictBlocks = 24576;
+// the longest block-table row an eviction takes (2 million tokens, four SMs)
+constexpr int kMaxEvictBlocks = 32768;
 
 cudaError_t launch_prompt(int dtype, const PromptParams &p, const uint16_t *q, int64_t q_stride, const uint16_t *k,
                           int64_t k_stride, int num_sms, cudaStream_t s);

@@ -9,14 +9,17 @@
 // rewritten as [kept, in order][entries past the length][evicted, in order],
 // a permutation of itself.
 //
-// One CTA per sequence, the row held on the SM (order-preserving integer keys
-// of the weights in registers, table and weights in shared memory), so every
-// output may be its input.  The smallest kept key is found by bits from the top, two at a
-// time: each round counts the keys at or above three thresholds, 16 rounds of
-// one barrier each whatever the weights are (a histogram by bytes would
-// serialise its atomics: weights of one sequence share their exponent bytes).
-// Two ordered scans over warp ballots then give every entry its place.  The
-// call is bound by latency: one 16384-page row is 192 KB of traffic.
+// One CTA per sequence, for long rows a cluster of four, an entry's key
+// (order-preserving integer of its weight), weight and page in registers, so
+// every output may be its input.  The smallest kept key is found a byte at a
+// time from the top: four histograms of the keys that share the bytes found so
+// far, each in eight copies by lane (weights of one sequence share their
+// exponents, and atomics on one address run one after the other), summed over
+// the cluster through distributed shared memory.  Ordered counts over warp
+// ballots then give every entry its place.  Bound by latency: the longest row is
+// 512 KB of traffic.
+#include <cooperative_groups.h>
+
 #include "kvq_around.h"
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
@@ -25,8 +28,8 @@ namespace kvq {
 
 namespace {
 
-constexpr int kEvictThreads = 1024;
-constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictCluster = 4;  // CTAs of a long row
+constexpr int kEvictCopies = 8;   // of a histogram
 
 // float -> uint32 whose unsigned order is the weight's order; NaN below
 // everything (as -inf), -0.0 equal to 0.0.  0 is free for "not a candidate".
@@ -49,158 +52,214 @@ __device__ __forceinline__ int inclusive_scan(int x, int lane)
 
 }  // namespace
 
-// Items are striped (item k of thread t is entry k * 1024 + t), so ballots of
-// item k, warp by warp, list the entries in order.
-template <int ITEMS>
-__global__ void __launch_bounds__(kEvictThreads, 1) evict_pages_kernel(EvictParams p)
+// CTA r of a row's CTAS has entries [r, r + 1) * THREADS * N, striped: item k of thread
+// t is entry k * THREADS + t of them, so ballots of item k, warp by warp, list the entries in order.
+template <int THREADS, int CTAS, int N>
+__global__ void __launch_bounds__(THREADS, 1) evict_pages_kernel(EvictParams p)
 {
-    extern __shared__ int32_t row[];                 // the table row, max_blocks entries, ...
-    float *w = reinterpret_cast<float *>(row + p.max_blocks);  // ... and the weights
-    __shared__ int32_t cnt[2][3][kEvictWarps];       // a round's counts by warp (double-buffered)
-    __shared__ int32_t before[ITEMS * kEvictWarps];  // entries counted before (item, warp) in its item
-    __shared__ int32_t total[32];                    // entries counted in an item
+    namespace cg = cooperative_groups;
+    constexpr int W = THREADS / 32;
+    __shared__ uint32_t hist[2][256 * kEvictCopies];  // a round's histogram in copies (two buffers in turn)
+    __shared__ uint32_t bins[2][256];                 // the CTA's sums of the copies
+    __shared__ __align__(16) uint32_t row_bins[2][256];  // the row's
+    __shared__ int32_t before[N][W];          // entries counted before (item, warp) in its item
+    __shared__ int32_t total[N];              // entries counted in an item
+    __shared__ int32_t cta_total[2][CTAS];    // entries counted by a CTA (for the ties, for the kept)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int b = blockIdx.x, mb = p.max_blocks;
+    const int b = blockIdx.x / CTAS, rank_cta = blockIdx.x % CTAS, mb = p.max_blocks;
     const int32_t *tin = p.table + (int64_t)b * mb;
     const float *win = p.weights + (int64_t)b * mb;
     int32_t *tout = p.table_out + (int64_t)b * mb;
     float *wout = p.weights_out + (int64_t)b * mb;
-    const int L = p.seq_lens[b];
-    const int64_t cap = (int64_t)mb * kPage;
-    const bool bad = L < 0 || L > cap;
+    const int e0 = rank_cta * THREADS * N + tid;  // item k is entry e0 + k * THREADS
+    if constexpr (CTAS > 1) cg::this_cluster().barrier_arrive();
+
+    // all loads at once: none waits for the length
+    const int L = p.seq_lens[b], want = p.keep[b];
+    int32_t page[N];
+    float w[N];
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        const int j = e0 + k * THREADS;
+        page[k] = j < mb ? tin[j] : 0;
+        w[k] = j < mb ? win[j] : 0.0f;
+    }
+    const bool bad = L < 0 || L > (int64_t)mb * kPage;
     if (bad && tid == 0) set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
     const int nb = bad ? mb : (L + kPage - 1) / kPage;  // (bad: the row is copied as it is)
-    const int budget = bad ? nb : max(0, min(p.keep[b], nb));
+    const int budget = bad ? nb : max(0, min(want, nb));
     const int lo = min(p.sink, nb), hi = max(lo, nb - max(p.recent, 1));  // candidates [lo, hi)
     const int guarded = nb - (hi - lo);
     const int room = min(hi - lo, max(0, budget - guarded));
-
-    uint32_t key[ITEMS];  // 0: no candidate
+    const bool some = room > 0 && room < hi - lo;  // (the same for the whole row)
+    uint32_t key[N];                               // 0: no candidate
 #pragma unroll
-    for (int k = 0; k < ITEMS; k++) {
-        const int j = k * kEvictThreads + tid;
-        key[k] = 0;
-        if (j < mb) {
-            row[j] = tin[j];  // (read again by this thread only)
-            const float x = j < nb ? win[j] : 0.0f;
-            w[j] = x;
-            if (j >= lo && j < hi) key[k] = weight_key(x);
-        }
+    for (int k = 0; k < N; k++) {
+        const int j = e0 + k * THREADS;
+        key[k] = j >= lo && j < hi ? weight_key(w[k]) : 0u;
     }
-    // T = the room-th largest candidate key: the largest T with #(key >= T) >= room
+    if constexpr (CTAS > 1) cg::this_cluster().barrier_wait();  // every CTA runs: its shared memory may be written
+
+    // T = the room-th largest candidate key, `ties` of those equal to it stay
     uint32_t T = 0;
-    int above = 0;  // #(key > T) once T is final
-    if (room > 0 && room < hi - lo) {
-        for (int sh = 30, r = 0; sh >= 0; sh -= 2, r ^= 1) {
-            int c1 = 0, c2 = 0, c3 = 0;
-            const uint32_t t1 = T + (1u << sh), t2 = T + (2u << sh), t3 = T + (3u << sh);
+    int ties = room;
+    if (some) {
+        for (int i = tid; i < 2 * 256 * kEvictCopies; i += THREADS) (&hist[0][0])[i] = 0u;
+        __syncthreads();
+#pragma unroll 1
+        for (int r = 0; r < 4; r++) {
+            const int sh = 24 - 8 * r, buf = r & 1;
 #pragma unroll
-            for (int k = 0; k < ITEMS; k++) {
-                c1 += key[k] >= t1;
-                c2 += key[k] >= t2;
-                c3 += key[k] >= t3;
+            for (int k = 0; k < N; k++)
+                if (key[k] && (r == 0 || key[k] >> (sh + 8) == T >> (sh + 8)))
+                    atomicAdd(&hist[buf][(key[k] >> sh & 255u) * kEvictCopies + lane % kEvictCopies], 1u);
+            __syncthreads();
+            for (int i = tid; i < 256; i += THREADS) {
+                uint32_t c = 0;
+#pragma unroll
+                for (int x = 0; x < kEvictCopies; x++) {
+                    c += hist[buf][i * kEvictCopies + x];
+                    hist[buf][i * kEvictCopies + x] = 0u;  // (written again two rounds on)
+                }
+                if constexpr (CTAS > 1)
+                    bins[buf][i] = c;
+                else
+                    row_bins[buf][i] = c;
             }
-            c1 = __reduce_add_sync(kFull, c1);
-            c2 = __reduce_add_sync(kFull, c2);
-            c3 = __reduce_add_sync(kFull, c3);
-            if (lane == 0) {
-                cnt[r][0][warp] = c1;
-                cnt[r][1][warp] = c2;
-                cnt[r][2][warp] = c3;
+            if constexpr (CTAS > 1) {
+                cg::cluster_group cluster = cg::this_cluster();
+                cluster.sync();
+                for (int i = tid; i < 256; i += THREADS) {
+                    uint32_t c = 0;
+#pragma unroll
+                    for (int x = 0; x < CTAS; x++) c += *cluster.map_shared_rank(&bins[buf][i], x);
+                    row_bins[buf][i] = c;
+                }
             }
             __syncthreads();
-            c1 = __reduce_add_sync(kFull, cnt[r][0][lane]);
-            c2 = __reduce_add_sync(kFull, cnt[r][1][lane]);
-            c3 = __reduce_add_sync(kFull, cnt[r][2][lane]);
-            T = c3 >= room ? t3 : c2 >= room ? t2 : c1 >= room ? t1 : T;
-        }
-        int c = 0;
+            // every warp: lane l holds bins 255 - 8 l .. 248 - 8 l; the bin where the count from the
+            // top reaches `ties`
+            const uint4 *v = reinterpret_cast<const uint4 *>(&row_bins[buf][248 - 8 * lane]);
+            const uint4 v0 = v[0], v1 = v[1];
+            const uint32_t c[8] = {v1.w, v1.z, v1.y, v1.x, v0.w, v0.z, v0.y, v0.x};
+            int sum = 0;
 #pragma unroll
-        for (int k = 0; k < ITEMS; k++) c += key[k] > T;
-        c = __reduce_add_sync(kFull, c);
-        if (lane == 0) cnt[0][0][warp] = c;
-        __syncthreads();
-        above = __reduce_add_sync(kFull, cnt[0][0][lane]);
+            for (int x = 0; x < 8; x++) sum += (int)c[x];
+            int run = inclusive_scan(sum, lane);
+            const int at = __ffs(__ballot_sync(kFull, run >= ties)) - 1;
+            run -= sum;
+            int digit = -1, left = 0;
+#pragma unroll
+            for (int x = 0; x < 8; x++) {
+                if (digit < 0 && run + (int)c[x] >= ties) {
+                    digit = 255 - 8 * lane - x;
+                    left = ties - run;
+                }
+                run += (int)c[x];
+            }
+            T |= (uint32_t)__shfl_sync(kFull, digit, at) << sh;
+            ties = __shfl_sync(kFull, left, at);
+        }
     }
-    // ordered counts of a predicate over the row: ballots by (item, warp), then one scan
-    int item0 = 0;  // lane k: entries counted before item k
-    auto count = [&](auto pred) {
+    // ordered counts of a predicate over the row: ballots by (item, warp), scans, the CTAs' totals
+    int base = 0, item0 = 0;  // entries counted in lower CTAs; lane k: before item k
+    auto count = [&](auto pred, int which) {
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < ITEMS; k++) {
+        for (int k = 0; k < N; k++) {
             const uint32_t m = __ballot_sync(kFull, pred(k));
-            if (lane == 0) before[k * kEvictWarps + warp] = __popc(m);
+            if (lane == 0) before[k][warp] = __popc(m);
         }
         __syncthreads();
-        if (warp < ITEMS) {  // warp k scans item k's counts, ...
-            const int c = before[warp * kEvictWarps + lane];
-            const int s = inclusive_scan(c, lane);
-            before[warp * kEvictWarps + lane] = s - c;
-            if (lane == 31) total[warp] = s;
+        for (int k = warp; k < N; k += W) {  // a warp scans an item's counts, ...
+            const int x = lane < W ? before[k][lane] : 0;
+            const int s = inclusive_scan(x, lane);
+            if (lane < W) before[k][lane] = s - x;
+            if (lane == 31) total[k] = s;
         }
         __syncthreads();
-        // ... and every warp the items' totals
-        const int tot = lane < ITEMS ? total[lane] : 0;
-        item0 = inclusive_scan(tot, lane) - tot;
+        const int x = lane < N ? total[lane] : 0;  // ... every warp the items' totals
+        const int s = inclusive_scan(x, lane);
+        item0 = s - x;
+        base = 0;
+        if constexpr (CTAS > 1) {
+            cg::cluster_group cluster = cg::this_cluster();
+            if (warp == 0 && lane < CTAS)
+                *cluster.map_shared_rank(&cta_total[which][rank_cta], lane) = __shfl_sync((1u << CTAS) - 1u, s, N - 1);
+            cluster.sync();
+            base = __reduce_add_sync(kFull, lane < rank_cta ? cta_total[which][lane] : 0);
+        }
     };
     // entries counted before item k of this thread (x: its own predicate)
     auto rank = [&](int k, bool x) {
-        return before[k * kEvictWarps + warp] + __shfl_sync(kFull, item0, k) +
+        return base + before[k][warp] + __shfl_sync(kFull, item0, k) +
                __popc(__ballot_sync(kFull, x) & ((1u << lane) - 1u));
     };
     const bool all = room >= hi - lo;
-    const int ties = room - above;  // keys equal to T that stay: the first of them
-    uint32_t kept = 0;  // bit k: item k stays
-    if (room > 0 && !all) count([&](int k) { return key[k] == T; });
+    uint32_t kept = 0;              // bit k: item k stays
+    if (some) count([&](int k) { return key[k] == T; }, 0);
 #pragma unroll
-    for (int k = 0; k < ITEMS; k++) {
-        const int j = k * kEvictThreads + tid;
+    for (int k = 0; k < N; k++) {
+        const int j = e0 + k * THREADS;
         bool stays = j < lo || j >= hi || all;
-        if (room > 0 && !all) {  // (the same for the whole CTA)
+        if (some) {
             const int r = rank(k, key[k] == T);
             stays = stays || key[k] > T || (key[k] == T && r < ties);
         }
         kept |= (uint32_t)(stays && j < nb) << k;
     }
-    count([&](int k) { return (kept >> k & 1u) != 0; });
+    // (every CTA of the row has read its entries by the barriers in here: the outputs may be the inputs)
+    count([&](int k) { return (kept >> k & 1u) != 0; }, 1);
     const int stay = guarded + room, gone = nb - stay;
 #pragma unroll
-    for (int k = 0; k < ITEMS; k++) {
-        const int j = k * kEvictThreads + tid;
+    for (int k = 0; k < N; k++) {
+        const int j = e0 + k * THREADS;
         const bool stays = (kept >> k & 1u) != 0;
         const int r = rank(k, stays);
         if (j >= mb) continue;
         if (stays) {
-            tout[r] = row[j];
-            wout[r] = w[j];
+            tout[r] = page[k];
+            wout[r] = w[k];
         } else {  // evicted: behind everything, in order; past the length: moves up
-            tout[j < nb ? mb - gone + (j - r) : j - gone] = row[j];
+            tout[j < nb ? mb - gone + (j - r) : j - gone] = page[k];
         }
         if (j >= stay) wout[j] = 0.0f;
     }
-    if (tid == 0) {
+    if (tid == 0 && rank_cta == 0) {
         p.seq_lens_out[b] = L - kPage * gone;
         p.num_evicted[b] = gone;
     }
+    if constexpr (CTAS > 1) cg::this_cluster().sync();  // no CTA ends while another may write to it
 }
 
-template <int ITEMS>
-static cudaError_t launch_evict_items(const EvictParams &p, cudaStream_t s)
+template <int THREADS, int CTAS, int N>
+static cudaError_t launch_evict_rows(const EvictParams &p, cudaStream_t s)
 {
-    const size_t smem = (size_t)p.max_blocks * (sizeof(int32_t) + sizeof(float));
-    cudaError_t e = cudaFuncSetAttribute(evict_pages_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(ITEMS * kEvictThreads * (sizeof(int32_t) + sizeof(float))));
-    if (e != cudaSuccess) return e;
-    return launch_plain(evict_pages_kernel<ITEMS>, dim3((unsigned)p.num_seqs), dim3(kEvictThreads), smem, s, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.num_seqs * CTAS);
+    cfg.blockDim = dim3(THREADS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CTAS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, evict_pages_kernel<THREADS, CTAS, N>, p);
 }
 
+// Few threads, many entries each: barriers cost more than instructions here.  A row of 16400
+// entries (16 rows, event time with a launch): one CTA of 1024 threads 28 us, clusters of eight
+// CTAs of 1024 / 256 threads 34 / 22 us, of four of 512 threads 20 us; rows of up to 512 entries
+// 10 us with 128 threads.
 cudaError_t launch_evict(const EvictParams &p, cudaStream_t s)
 {
-    static_assert(kMaxEvictBlocks == 24 * kEvictThreads, "the longest row fits the largest instance");
-    if (p.max_blocks <= kEvictThreads) return launch_evict_items<1>(p, s);
-    if (p.max_blocks <= 4 * kEvictThreads) return launch_evict_items<4>(p, s);
-    if (p.max_blocks <= 16 * kEvictThreads) return launch_evict_items<16>(p, s);
-    return launch_evict_items<24>(p, s);
+    static_assert(kMaxEvictBlocks == 512 * 16 * kEvictCluster, "the longest row fits the largest instance");
+    if (p.max_blocks <= 128 * 4) return launch_evict_rows<128, 1, 4>(p, s);
+    if (p.max_blocks <= 512 * 8) return launch_evict_rows<512, 1, 8>(p, s);
+    if (p.max_blocks <= 512 * 9 * kEvictCluster) return launch_evict_rows<512, kEvictCluster, 9>(p, s);
+    return launch_evict_rows<512, kEvictCluster, 16>(p, s);
 }
 
 }  // namespace kvq

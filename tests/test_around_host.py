@@ -78,7 +78,7 @@ def test_evict_pages_refusals():
         return f(bt, mb, lens, w, n, keep, sink, recent, to, lo, wo, gone, None, None)
 
     assert call(n=-1) == 1 and call(mb=0) == 1 and call(sink=-1) == 1 and call(recent=-1) == 1
-    assert call(mb=24577) == 2
+    assert call(mb=32769) == 2 and call(n=(1 << 27) + 1) == 2
     assert call(n=0, bt=None, lens=None, w=None, keep=None, to=None, lo=None, wo=None, gone=None) == 0
     for name in ("bt", "lens", "w", "keep", "to", "lo", "wo", "gone"):
         assert call(**{name: None}) == 1, name

@@ -55,7 +55,7 @@ def test_ragged_rows(cuda_ok, sink, recent, in_place):
         _check(table, lens, w, _i32(keep), sink, recent, in_place=in_place)
 
 
-@pytest.mark.parametrize("mb", [1, 1023, 1024, 1025, 4096, 4097, 16384, 16385, 24576])
+@pytest.mark.parametrize("mb", [1, 127, 128, 129, 511, 512, 513, 1023, 1024, 1025, 4096, 4097, 16385, 18432, 18433, 32768])
 def test_row_lengths_around_the_instances(cuda_ok, mb):
     """Rows as long as each instance of the kernel takes, and one more; full and nearly full."""
     table, lens, w = _case(2, [mb, max(1, mb - 3), mb // 2 + 1], 0)
@@ -102,7 +102,7 @@ def test_empty_batch_and_refusals(cuda_ok):
     z = torch.zeros(0, 4, dtype=torch.int32, device="cuda")
     e = _i32([])
     kvq.kvq_evict_pages(z, e, z.float(), e, 1, 1, z.clone(), e.clone(), z.float(), e.clone())
-    big = torch.zeros(1, 24577, dtype=torch.int32, device="cuda")
+    big = torch.zeros(1, 32769, dtype=torch.int32, device="cuda")
     with pytest.raises(kvq.KvqError) as err:
         kvq.kvq_evict_pages(big, _i32([1]), big.float(), _i32([1]), 1, 1, big, _i32([1]), big.float(), _i32([1]))
     assert err.value.status == 2
