@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_pages_kernel(EvictParams p)
         const int j = e0 + k * THREADS;
         key[k] = j >= lo && j < hi ? weight_key(w[k]) : 0u;
     }
+    __syncwarp();
     if constexpr (CTAS > 1) cg::this_cluster().barrier_wait();  // every CTA runs: its shared memory may be written
 
     // T = the room-th largest candidate key, `ties` of those equal to it stay
@@ -128,6 +129,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_pages_kernel(EvictParams p)
             }
             if constexpr (CTAS > 1) {
                 cg::cluster_group cluster = cg::this_cluster();
+                __syncwarp();
                 cluster.sync();
                 for (int i = tid; i < 256; i += THREADS) {
                     uint32_t c = 0;
@@ -184,8 +186,9 @@ __global__ void __launch_bounds__(THREADS, 1) evict_pages_kernel(EvictParams p)
         base = 0;
         if constexpr (CTAS > 1) {
             cg::cluster_group cluster = cg::this_cluster();
-            if (warp == 0 && lane < CTAS)
-                *cluster.map_shared_rank(&cta_total[which][rank_cta], lane) = __shfl_sync((1u << CTAS) - 1u, s, N - 1);
+            const int mine = __shfl_sync(kFull, s, N - 1);  // (by every lane: lane N - 1 holds the CTA's sum)
+            if (warp == 0 && lane < CTAS) *cluster.map_shared_rank(&cta_total[which][rank_cta], lane) = mine;
+            __syncwarp();
             cluster.sync();
             base = __reduce_add_sync(kFull, lane < rank_cta ? cta_total[which][lane] : 0);
         }
@@ -229,7 +232,10 @@ __global__ void __launch_bounds__(THREADS, 1) evict_pages_kernel(EvictParams p)
         p.seq_lens_out[b] = L - kPage * gone;
         p.num_evicted[b] = gone;
     }
-    if constexpr (CTAS > 1) cg::this_cluster().sync();  // no CTA ends while another may write to it
+    if constexpr (CTAS > 1) {
+        __syncwarp();
+        cg::this_cluster().sync();  // no CTA ends while another may write to it
+    }
 }
 
 template <int THREADS, int CTAS, int N>
