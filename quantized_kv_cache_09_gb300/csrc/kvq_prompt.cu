@@ -32,8 +32,9 @@
 //             M = N = 128.  (An MMA holds its issuer until the tensor pipe takes it,
 //             and a wait between MMAs costs ~100 cycles: with one thread for both
 //             tiles the pipe was busy 49% of the time.)
-//   13        walks the unit list and issues the TMA copies: Q tiles and a ring
-//             of five 32 KB stages, K and V alternating.
+//   13        walks the unit list and issues the copies of K and V (TMA) into a
+//             ring of five 32 KB stages.
+//   15        issues the copies of the Q tiles.
 // While one tile's rows are in the softmax, the tensor cores work on the other.
 //
 // Unit order: by the number of the unit in its sequence, the highest (most
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(&sm.unit_full[s], 1);
-            mbar_init(&sm.unit_free[s], 14);  // 8 softmax warps, 4 epilogue warps, 2 MMA threads
+            mbar_init(&sm.unit_free[s], 15);  // 8 softmax warps, 4 epilogue warps, 2 MMA threads, the Q thread
         }
         mbar_init(&sm.mma_done, 2);
         mbar_init_fence();
@@ -425,36 +426,40 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             wild = epilogue_any(wild);
             for (int t = 0; t < sp.active && ok; t++) {
-                ok = __all_sync(kFull, mbar_wait_bounded(&sm.ml_full[t], done[t] & 1u) &&
-                                           mbar_wait_bounded(&sm.o_full[t], done[t] & 1u));
+                ok = __all_sync(kFull, mbar_wait_bounded(&sm.ml_full[t], done[t] & 1u));
                 if (!ok) break;
-                done[t]++;
-                tc_fence_after();
                 const float2 ml = sm.ml[t][row];
                 const float inv = 1.0f / ml.y;
                 const int tok = u.tok0 + t * p.tile1_token + row / th, hq = u.h * G + t * p.tile1_head + row % th;
                 const bool live = row < th * tt && tok < u.n;
+                ok = __all_sync(kFull, mbar_wait_bounded(&sm.o_full[t], done[t] & 1u));
+                if (!ok) break;
+                done[t]++;
+                tc_fence_after();
                 const int64_t at = (int64_t)(u.c0 + tok) * p.num_q_heads + hq;
                 uint32_t o[64];
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t x[32];
-                    tmem_ld32_async(lane_tm + 256 * t + 128 + 32 * c, x);
+                for (int c = 0; c < 2; c++) {
+                    uint32_t x[2][32];
+                    tmem_ld32_async(lane_tm + 256 * t + 128 + 64 * c, x[0]);
+                    tmem_ld32_async(lane_tm + 256 * t + 128 + 64 * c + 32, x[1]);
                     tmem_ld_wait();
                     if (wild && live) {
                         // values that are not finite, of the keys this row sees in the mixed steps
                         for (int j = sp.mixed * kKeys; j <= tok; j++) {
-                            const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + 32 * c;
+                            const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + 64 * c;
 #pragma unroll
-                            for (int e = 0; e < 32; e++) {
+                            for (int e = 0; e < 64; e++) {
                                 const float y = E::value(vr[e]);
-                                if (!(fabsf(y) < INFINITY)) x[e] = __float_as_uint(__uint_as_float(x[e]) + y);
+                                uint32_t &z = x[e >> 5][e & 31];
+                                if (!(fabsf(y) < INFINITY)) z = __float_as_uint(__uint_as_float(z) + y);
                             }
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        o[16 * c + e] = E::pack(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+                    for (int e = 0; e < 32; e++)
+                        o[32 * c + e] = E::pack(__uint_as_float(x[e >> 4][2 * (e & 15)]) * inv,
+                                                __uint_as_float(x[e >> 4][2 * (e & 15) + 1]) * inv);
                 }
                 // O may be written again before this one's stores, which take far longer than its loads
                 tc_fence_before();
@@ -603,7 +608,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             uint32_t used = 0;  // stages filled so far, up to kStages
             // bit s: parity of stage s's next kv_full, kv_raw; whether its last fill was a mixed V
             uint32_t full_phase = 0, raw_phase = 0, last_raw = 0;
-            uint32_t uses[kUnitTiles] = {0, 0};
             for (int r = 0;; r++) {
                 const int64_t id = (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 while (x >= 0 && id >= base + (int64_t)count * H) {
@@ -657,15 +661,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     };
                     for (int i = 0; i < sp.total && ok; i++) {
                         stage(&map_k, i * kKeys, false);
-                        for (int t = 0; i == 0 && t < sp.active && ok; t++) {
-                            if (uses[t] > 0) ok = mbar_wait_bounded(&sm.q_free[t], (uses[t] - 1) & 1u);
-                            if (!ok) break;
-                            mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * th * tt);
-                            const int tok = u.c0 + u.tok0 + t * p.tile1_token, hq = u.h * G + t * p.tile1_head;
-                            tma_load_3d(sm.q[t], &map_q, 0, hq, tok, &sm.q_full[t]);
-                            tma_load_3d(sm.q[t] + kTileBytes / 2, &map_q, 64, hq, tok, &sm.q_full[t]);
-                            uses[t]++;
-                        }
                         if (ok) stage(&map_v, i * kKeys, i >= sp.mixed);
                     }
                 }
@@ -678,9 +673,30 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     const uint32_t next = (raw ? raw_phase : full_phase) >> s & 1u;
                     if (!mbar_wait_bounded(raw ? &sm.kv_raw[s] : &sm.kv_full[s], next ^ 1u)) ok = false;
                 }
-                for (int t = 0; t < kUnitTiles; t++)
-                    if (uses[t] > 0 && !mbar_wait_bounded(&sm.q_full[t], (uses[t] - 1) & 1u)) ok = false;
             }
+        } else if (warp == 15 && lane == 0) {
+            // ---- Q tiles: apart from K and V, whose copies would wait behind a tile in use ----
+            uint32_t uses[kUnitTiles] = {0, 0};
+            for (int r = 0; ok; r++) {
+                PromptUnit u;
+                if (!fetch(r, u)) break;
+                mbar_arrive(&sm.unit_free[r & 1]);
+                if (u.n < 0) break;
+                const Span sp(u, p);
+#pragma unroll
+                for (int t = 0; t < kUnitTiles; t++) {
+                    if (t >= sp.active || !ok) continue;
+                    if (uses[t] > 0) ok = mbar_wait_bounded(&sm.q_free[t], (uses[t] - 1) & 1u);
+                    if (!ok) continue;
+                    mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * th * tt);
+                    const int tok = u.c0 + u.tok0 + t * p.tile1_token, hq = u.h * G + t * p.tile1_head;
+                    tma_load_3d(sm.q[t], &map_q, 0, hq, tok, &sm.q_full[t]);
+                    tma_load_3d(sm.q[t] + kTileBytes / 2, &map_q, 64, hq, tok, &sm.q_full[t]);
+                    uses[t]++;
+                }
+            }
+            for (int t = 0; t < kUnitTiles; t++)  // no copy in flight when the CTA ends
+                if (uses[t] > 0 && !mbar_wait_bounded(&sm.q_full[t], (uses[t] - 1) & 1u)) ok = false;
         }
     }
     __syncwarp();
