@@ -197,8 +197,9 @@ size_t kvq_decode_workspace_bytes(kvq_format fmt, int32_t num_heads, int32_t hea
  *                    of a call that set any KVQ_FLAG_* bit are undefined
  * Launch: with programmatic dependent launch, the kernel starts while the
  * previous kernel of the stream finishes and reads seq_lens and block_table
- * before waiting for it (the codes, scales, q and out only after).  No kvq_*
- * call writes those two arrays; a caller's own kernel that writes them right
+ * before waiting for it (the codes, scales, q and out only after).  Of the
+ * kvq_* calls only kvq_evict_pages writes those two arrays, by an ordinary
+ * launch; a caller's own kernel that writes them right
  * before this call must not trigger its dependents early
  * (griddepcontrol.launch_dependents) -- ordinary launches never do.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED, KVQ_ERR_WORKSPACE,
@@ -375,6 +376,10 @@ kvq_status kvq_prompt_attention(kvq_dtype dtype, const uint16_t *q, int64_t q_ro
  *   workspace        >= kvq_page_weights_workspace_bytes(...) bytes, 16-byte
  *                    aligned, any contents.  Do not share one workspace
  *                    between calls that may run concurrently.
+ * Launch: with programmatic dependent launch; cu_seqlens_q, seq_lens and
+ * block_table are read before waiting for the previous kernel of the stream,
+ * everything else after; the same condition as for kvq_decode_attention's
+ * seq_lens and block_table holds for these three.
  * A sequence that breaks a bound is skipped (its row stays as it was) and
  * KVQ_FLAG_BAD_LENGTH set; a block-table entry out of range sets
  * KVQ_FLAG_BAD_PAGE (page 0 is read instead).  Errors: KVQ_ERR_INVALID_ARG,

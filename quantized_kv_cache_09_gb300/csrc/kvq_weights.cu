@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     if (lane < kPwStages) mbar_init(&sm.full[warp][lane], 1);
     mbar_init_fence();
     // units of sequence b: (cache head, block of kCols query rows, page), the page fastest
+    bool bad_seq = false, bad_page = false;
     if (warp == 0) {
         int64_t run = 0;
         for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
@@ -113,8 +114,8 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
                 PwSeq s;
                 if (pw_seq(p, b0 + lane, s))
                     u = (int64_t)((s.L + kPage - 1) / kPage) * H * (((int64_t)s.n * G + kCols - 1) / kCols);
-                else if (blockIdx.x == 0)
-                    set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
+                else
+                    bad_seq = true;
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -163,19 +164,23 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     uint32_t ph[2] = {0u, 0u};
     float sk[2] = {0.0f, 0.0f};
     int pj[2] = {0, 0};
-    auto look = [&](int i, uint32_t &ph_, float &sk_, int &pj_) {
+    auto look = [&](int i, uint32_t &ph_, int &pj_) {
         if (i + lane >= units) return;
         const Place x = place(first + i + lane);
         int pg = p.block_table[(int64_t)x.b * p.max_blocks + x.j];
         if (pg < 0 || pg >= p.num_pages) {
-            set_flag(p.status, KVQ_FLAG_BAD_PAGE);
+            bad_page = true;
             pg = 0;
         }
         ph_ = (uint32_t)pg * (uint32_t)H + (uint32_t)x.h;
-        sk_ = p.k_scales[ph_];
         pj_ = x.j;
     };
-    look(0, ph[0], sk[0], pj[0]);
+    auto scales = [&](int i, uint32_t ph_, float &sk_) {
+        if (i + lane < units) sk_ = p.k_scales[ph_];
+    };
+    look(0, ph[0], pj[0]);
+    pdl_wait();  // (the lengths and the block table are read before it, everything else after)
+    if (bad_seq && blockIdx.x == 0) set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
     const int chunks = units * F::kChunks;
     uint8_t *ring = sm.ring[warp][0];
     uint64_t *full = sm.full[warp];
@@ -194,7 +199,9 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     };
     __syncwarp();
     for (int c = 0; c < kPwStages; c++) bring(c);
-    look(32, ph[1], sk[1], pj[1]);
+    scales(0, ph[0], sk[0]);
+    look(32, ph[1], pj[1]);
+    scales(32, ph[1], sk[1]);
 
     uint32_t qb[NT][8][2];       // the unit's query rows as the B operand: column g of tile nt is row row0 + 8 nt + g
     float bias[NT][2];           // columns 2t, 2t + 1: minus the offset share of every raw score (int4)
@@ -207,10 +214,13 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     uint32_t phase = 0;
     for (int i = 0; i < units; i++) {
         if (i > 0 && (i & 31) == 0) {  // this ring's turn: the other looks 32 units ahead of it
-            if (i & 32)
-                look(i + 32, ph[0], sk[0], pj[0]);
-            else
-                look(i + 32, ph[1], sk[1], pj[1]);
+            if (i & 32) {
+                look(i + 32, ph[0], pj[0]);
+                scales(i + 32, ph[0], sk[0]);
+            } else {
+                look(i + 32, ph[1], pj[1]);
+                scales(i + 32, ph[1], sk[1]);
+            }
         }
         float fac;
         int j;
@@ -402,6 +412,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
             if (g < 2 && d) d[j] = fmaf(f, mm, FMT == KVQ_INT4_B64 ? bb * fac : 0.0f) + __log2f(l);
         }
     }
+    if (bad_page) set_flag(p.status, KVQ_FLAG_BAD_PAGE);
     if (!ok) {  // a copy did not come: flagged, and none is left in flight
         if (lane == 0) set_flag(p.status, KVQ_FLAG_TIMEOUT);
         for (int k = 0; k < kPwStages && c + k < chunks; k++) {
@@ -535,7 +546,7 @@ static cudaError_t launch_page_lse(const PageWeightsParams &p, int num_sms, cuda
     cudaError_t e = cudaFuncSetAttribute(page_lse_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(PwSmem));
     if (e != cudaSuccess) return e;
-    return launch_plain(page_lse_kernel<FMT, NT>, dim3((unsigned)num_sms), dim3(kPwWarps * 32), sizeof(PwSmem), s, p);
+    return launch_pdl(page_lse_kernel<FMT, NT>, dim3((unsigned)num_sms), dim3(kPwWarps * 32), sizeof(PwSmem), s, p);
 }
 
 template <int FMT>

@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     // steps of sequence b: (cache head, tile of query rows, page pair), the pages fastest
     auto steps_of = [&](const PwSeq &s) { return (s.L + kWinKeys - 1) / kWinKeys; };
     auto tiles_of = [&](const PwSeq &s) { return (s.n * G + kWinRows - 1) / kWinRows; };
+    bool bad_seq = false;
     if (warp == 13) {
         int64_t run = 0;
         for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
@@ -150,8 +151,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 PwSeq s;
                 if (pw_seq(p, b0 + lane, s))
                     u = (int64_t)steps_of(s) * H * tiles_of(s);
-                else if (blockIdx.x == 0)
-                    set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
+                else
+                    bad_seq = true;
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -166,6 +167,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait();  // (the lengths are read before it, everything else after)
+    if (bad_seq && blockIdx.x == 0) set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
     const uint32_t tmem = sm.tmem;
     // step u of the launch: its sequence; of it the step's record, but for the scales and flags; and
     // its number among the tile's `all` steps
@@ -440,7 +443,7 @@ static cudaError_t launch_page_window_fmt(const PageWeightsParams &p, int num_sm
     cudaError_t e = cudaFuncSetAttribute(page_window_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(WinSmem));
     if (e != cudaSuccess) return e;
-    return launch_plain(page_window_kernel<FMT>, dim3((unsigned)num_sms), dim3(kWinThreads), sizeof(WinSmem), s, p);
+    return launch_pdl(page_window_kernel<FMT>, dim3((unsigned)num_sms), dim3(kWinThreads), sizeof(WinSmem), s, p);
 }
 
 cudaError_t launch_page_window(int fmt, const PageWeightsParams &p, int num_sms, cudaStream_t s)
