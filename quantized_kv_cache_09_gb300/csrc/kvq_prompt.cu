@@ -17,24 +17,26 @@
 // steps of 128.
 //
 // Roles (warps), handing over through mbarriers:
-//   0-3, 4-7  softmax of tile 0, tile 1: one thread per query row.  A row of S
+//   0, 2      one thread each issues the MMAs of a tile: S = Q K^T, O += P V,
+//             M = N = 128.  (An MMA holds its issuer until the tensor pipe takes it,
+//             and a wait between MMAs costs ~100 cycles: with one thread for both
+//             tiles the pipe was busy 49% of the time.  The scheduler favours the
+//             lower warps, and these few instructions are the ones that others
+//             wait for: behind the softmax they were late by hundreds of cycles.)
+//   1         walks the unit list and issues the copies of K and V (TMA) into a
+//             ring of five 32 KB stages.
+//   3         issues the copies of the Q tiles.
+//   4-7, 8-11 softmax of tile 0, tile 1: one thread per query row.  A row of S
 //             (128 scores) is read into registers once; maximum, 2^(s - m), the
 //             row sum in binary32; P rounded to the operands' type (the tensor
-//             cores take nothing wider) goes over S in two halves.  The running
+//             cores take nothing wider) goes over S in three parts.  The running
 //             maximum is lazy: O is rescaled only when a row's maximum grows by
 //             more than 2^8, so P stays in [0, 256].
-//   8-11      the last step(s) of a unit hold keys past some row's position:
+//   12-15     the last step(s) of a unit hold keys past some row's position:
 //             their V rows past the sequence's end are zeroed and values that
 //             are not finite taken out (0 * inf would reach rows that do not see
 //             them; the epilogue adds them to the rows that do).  Then the
 //             epilogue: O / l, while the tensor cores are on the next unit.
-//   12, 14    one thread each issues the MMAs of a tile: S = Q K^T, O += P V,
-//             M = N = 128.  (An MMA holds its issuer until the tensor pipe takes it,
-//             and a wait between MMAs costs ~100 cycles: with one thread for both
-//             tiles the pipe was busy 49% of the time.)
-//   13        walks the unit list and issues the copies of K and V (TMA) into a
-//             ring of five 32 KB stages.
-//   15        issues the copies of the Q tiles.
 // While one tile's rows are in the softmax, the tensor cores work on the other.
 //
 // Unit order: by the number of the unit in its sequence, the highest (most
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         mbar_init(&sm.mma_done, 2);
         mbar_init_fence();
     }
-    if (warp == 12) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)),
                      "r"(kPromptTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -252,10 +254,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         return ok;
     };
 
-    if (warp < 8) {
+    if (warp >= 4 && warp < 12) {
         // ---- softmax: tile t, one query row per thread (its lane of tensor memory) ----
         regs_inc<kRegsSoftmax>();
-        const int t = warp >> 2, row = tid & 127;
+        const int t = (warp >> 2) - 1, row = tid & 127;
         const uint32_t tm = tmem + 256u * t + ((uint32_t)((warp & 3) * 32) << 16);
         const float sabs = fmaxf(fabsf(p.score_scale), kMinScale);
         uint32_t s_phase = 0, done = 0;  // steps of this tile, units of this tile
@@ -373,10 +375,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             if (lane == 0) mbar_arrive(&sm.ml_full[t]);
             done++;
         }
-    } else if (warp < 12) {
+    } else if (warp >= 12) {
         // ---- V of the mixed steps, then the epilogue ----
         regs_dec<kRegsEpilogue>();
-        const int w = tid - 256, row = w;
+        const int w = tid & 127, row = w;
         const uint32_t lane_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         Ring ring;
         uint32_t raw_phase = 0;  // bit s: parity of stage s's next mixed V
@@ -474,9 +476,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
     } else {
         regs_dec<kRegsIssue>();
-        if (warp != 13 && warp - 12 <= 2 && lane == 0) {
-            // ---- the MMA thread of tile t (warps 12 and 14) ----
-            const int t = (warp - 12) >> 1;
+        if ((warp & 1) == 0 && lane == 0) {
+            // ---- the MMA thread of tile t (warps 0 and 2) ----
+            const int t = warp >> 1;
             const uint32_t tm = tmem + 256 * t;
             const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.q[0])) >> 32);
             const uint32_t hi_v = (uint32_t)(umma_desc_mn(smem_addr(sm.kv[0]), kKeys * 128, 1024) >> 32);
@@ -580,7 +582,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
             if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
-        } else if (warp == 13) {
+        } else if (warp == 1) {
             // ---- units and copies ----
             const int H = p.num_heads, ut = p.unit_tokens;
             // a sequence's length, 0 where its bounds are broken
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (!mbar_wait_bounded(raw ? &sm.kv_raw[s] : &sm.kv_full[s], next ^ 1u)) ok = false;
                 }
             }
-        } else if (warp == 15 && lane == 0) {
+        } else if (warp == 3 && lane == 0) {
             // ---- Q tiles: apart from K and V, whose copies would wait behind a tile in use ----
             uint32_t uses[kUnitTiles] = {0, 0};
             for (int r = 0; ok; r++) {
@@ -703,7 +705,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     if (!ok) set_flag(p.status, KVQ_FLAG_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 12)
+    if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kPromptTmem));
 }
 

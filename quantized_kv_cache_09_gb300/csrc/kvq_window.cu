@@ -6,13 +6,15 @@
 //
 // A persistent CTA per SM takes an equal contiguous share of all steps; a step is two pages (128
 // keys) of one (sequence, cache head, tile of 128 query rows).  Roles:
-//   warps 0-3    widening: codes of a step from the copy ring to fp16 in shared memory (128-byte
-//                swizzled, K-major); a new tile's query rows first, in the same layout.  int4 pairs
-//                come out as elements (0,4) (1,5) (2,6) (3,7) of a word, so q is permuted alike
-//   warps 4-11   softmax sums, warps 4-7 the even steps, 8-11 the odd ones: one thread per query
+//   warp 0       one thread issues the MMAs: S = Q K^T, M = N = 128, Q (two tiles) and three S in
+//                tensor memory (the lowest warp: the scheduler favours it, and all wait for it)
+//   warp 1       looks pages up and issues the bulk copies, five steps ahead
+//   warps 2-5    the next tile's query rows into tensor memory, a row per thread
+//   warps 6-9    widening: codes of a step from the copy ring to fp16 in shared memory (128-byte
+//                swizzled, K-major).  int4 pairs come out as elements (0,4) (1,5) (2,6) (3,7) of a
+//                word, and q is permuted alike
+//   warps 10-17  softmax sums, warps 10-13 the even steps, 14-17 the odd ones: one thread per query
 //                row reads its 64 scores of each page from tensor memory
-//   warp 12      one thread issues the MMAs: S = Q K^T, M = N = 128, four S in tensor memory
-//   warp 13      looks pages up and issues the bulk copies, five steps ahead
 // Every hand-off is an mbarrier, every wait bounded.  With 128 live rows a step costs about as
 // many cycles of the exponential unit (16384 / 32), of the tensor pipe (8 * 64) and of issue.
 #include "kvq_tc.cuh"
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
         mbar_init(&sm.mma_done, 1);
         mbar_init_fence();
     }
-    if (warp == 12) {
+    if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem)),
                      "r"(kWinTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     auto steps_of = [&](const PwSeq &s) { return (s.L + kWinKeys - 1) / kWinKeys; };
     auto tiles_of = [&](const PwSeq &s) { return (s.n * G + kWinRows - 1) / kWinRows; };
     bool bad_seq = false;
-    if (warp == 13) {
+    if (warp == 1) {
         int64_t run = 0;
         for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
             int64_t u = 0;
@@ -201,8 +203,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     const int steps = (int)(U * (blockIdx.x + 1) / gridDim.x - first);
     bool ok = true;
 
-    if (warp < 4) {
+    if (warp >= 6 && warp < 10) {
         // ---- widening ----
+        const int wt = tid - 6 * 32;
         Turn<kCodeStages> code;
         Turn<kKeyStages> key;
         for (int i = 0; i < steps; i++, code.next(), key.next()) {
@@ -211,10 +214,10 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             // int4: 8 threads take 4 keys x 2 pieces (16 bytes of a row), else 2 keys x 4 pieces: the
             // stores meet no bank conflict
             auto key_of = [&](int r) {
-                return RB == 64 ? (r >> 1) * kPage + 4 * (tid >> 3) + ((tid & 7) >> 1)
-                                : 32 * (r >> 1) + 2 * (tid >> 3) + ((tid & 7) >> 2);
+                return RB == 64 ? (r >> 1) * kPage + 4 * (wt >> 3) + ((wt & 7) >> 1)
+                                : 32 * (r >> 1) + 2 * (wt >> 3) + ((wt & 7) >> 2);
             };
-            auto piece_of = [&](int r) { return RB == 64 ? (tid & 1) + 2 * (r & 1) : (tid & 3) + 4 * (r & 1); };
+            auto piece_of = [&](int r) { return RB == 64 ? (wt & 1) + 2 * (r & 1) : (wt & 3) + 4 * (r & 1); };
             uint4 w[kLd];
 #pragma unroll
             for (int r = 0; r < kLd; r++) w[r] = *reinterpret_cast<const uint4 *>(sm.code[code.stage] + key_of(r) * RB + 16 * piece_of(r));
@@ -248,13 +251,13 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 mbar_arrive(&sm.code_free[code.stage]);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp >= 10) {
         // ---- softmax sums: one query row per thread ----
         const int row = (warp & 3) * 32 + lane;
         const float sabs = fmaxf(fabsf(p.score_scale), kPwMinScale);
         Turn<kScoreStages> score;
         for (int i = 0; i < steps; i++, score.next()) {
-            if ((i & 1) != (warp - 4) >> 2) continue;
+            if ((i & 1) != (warp - 10) >> 2) continue;
             const uint32_t ss = score.stage;
             ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[ss], score.parity));
             if (!ok) break;
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 if (hh < m.pages && rr < m.n * G) dst[hh] = f * mx + __log2f(la + lb);
             }
         }
-    } else if (warp == 12) {
+    } else if (warp == 0) {
         if (lane == 0) {
             // ---- the MMA thread ----
             const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.k[0])) >> 32);
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
             if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
         }
-    } else if (warp == 13) {
+    } else if (warp == 1) {
         // ---- pages and copies: lane l looks up step l of 32, two rings in turn ----
         WinStep ring[2];
         uint32_t ph[2][2];
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     if (!ok) set_flag(p.status, KVQ_FLAG_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 12)
+    if (warp == 0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kWinTmem));
 }
 
