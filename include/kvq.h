@@ -345,7 +345,7 @@ size_t kvq_prefill_workspace_bytes(int32_t num_q_heads, int32_t num_seqs, int32_
  *                    for instance), or NULL
  * A sequence that breaks a bound is skipped and KVQ_FLAG_BAD_LENGTH set.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (head_dim != 128, unknown
- * dtype, g > 128, more than 65535 sequences, total_tokens above 2^31 - 1),
+ * dtype, g > 128, more than 65535 sequences or cache heads, total_tokens above 2^31 - 1),
  * KVQ_ERR_CUDA.
  */
 kvq_status kvq_prompt_attention(kvq_dtype dtype, const uint16_t *q, int64_t q_row_stride, const uint16_t *k,

@@ -277,7 +277,8 @@ kvq_status kvq_prompt_attention(kvq_dtype dtype, const uint16_t *q, int64_t q_ro
     if (q_row_stride < q_row || k_row_stride < kv_row || v_row_stride < kv_row) return KVQ_ERR_INVALID_ARG;
     if (q_row_stride % 8 || k_row_stride % 8 || v_row_stride % 8) return KVQ_ERR_INVALID_ARG;
     const int g = num_q_heads / num_kv_heads;
-    if (g > kvq::kMaxPromptGroup || num_seqs > 65535 || total_tokens > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
+    if (g > kvq::kMaxPromptGroup || num_seqs > 65535 || num_kv_heads > 65535 || total_tokens > INT32_MAX)
+        return KVQ_ERR_UNSUPPORTED;
     // a row's bytes are a 40-bit stride of a tensor map
     const int64_t widest = q_row_stride > k_row_stride ? q_row_stride : k_row_stride;
     if ((widest > v_row_stride ? widest : v_row_stride) >= (int64_t)1 << 39) return KVQ_ERR_UNSUPPORTED;

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 
     // the r-th unit of this CTA, for every role but the loader's
     auto fetch = [&](int r, PromptUnit &u) {
-        ok = mbar_wait_bounded(&sm.unit_full[r & 1], (uint32_t)(r >> 1) & 1u);
+        ok = mbar_wait_short(&sm.unit_full[r & 1], (uint32_t)(r >> 1) & 1u);
         if (ok) u = sm.unit[r & 1];
         return ok;
     };
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             float m_used = -INFINITY;
             uint64_t l2 = pk2(0.0f, 0.0f);
             for (int i = 0; i < nst; i++) {
-                ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[t], s_phase & 1u));
+                ok = __all_sync(kFull, mbar_wait_short(&sm.s_full[t], s_phase & 1u));
                 s_phase++;
                 if (!ok) break;
                 tc_fence_after();
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             }
             if (!ok) break;
             // the epilogue has read the unit before's ml
-            if (done > 0) ok = __all_sync(kFull, mbar_wait_bounded(&sm.o_free[t], (done - 1) & 1u));
+            if (done > 0) ok = __all_sync(kFull, mbar_wait_short(&sm.o_free[t], (done - 1) & 1u));
             if (!ok) break;
             float la, lb;
             upk2(l2, la, lb);
@@ -399,26 +399,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             for (int i = 0; i < sp.total && ok; i++) {
                 ring.next();
                 if (i >= sp.mixed) {
-                    ok = __all_sync(kFull, mbar_wait_bounded(&sm.kv_raw[ring.stage], raw_phase >> ring.stage & 1u));
+                    ok = __all_sync(kFull, mbar_wait_short(&sm.kv_raw[ring.stage], raw_phase >> ring.stage & 1u));
                     if (!ok) break;
                     raw_phase ^= 1u << ring.stage;
                     uint8_t *v = sm.kv[ring.stage];
                     const int left = u.n - i * kKeys;  // keys of the step inside the sequence
+                    uint4 *piece = reinterpret_cast<uint4 *>(v);
+                    auto key_of = [](int e) { return (e & 1023) >> 3; };  // 8 pieces a key, two halves of the elements
+                    uint32_t odd = 0;
 #pragma unroll 4
                     for (int e = w; e < kTileBytes / 16; e += 128) {
-                        uint4 x = reinterpret_cast<const uint4 *>(v)[e];
-                        if ((e & 1023) >> 3 >= left) {  // (8 pieces a key in each half of the elements)
-                            reinterpret_cast<uint4 *>(v)[e] = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (E::wild(x.x) | E::wild(x.y) | E::wild(x.z) | E::wild(x.w)) {
-                            wild = true;
-                            uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
+                        const uint4 x = piece[e];
+                        if (key_of(e) >= left)
+                            piece[e] = make_uint4(0u, 0u, 0u, 0u);
+                        else
+                            odd |= E::wild(x.x) | E::wild(x.y) | E::wild(x.z) | E::wild(x.w);
+                    }
+                    if (odd) {
+                        wild = true;
+                        uint32_t *word = reinterpret_cast<uint32_t *>(v);
+#pragma unroll 1
+                        for (int e = w; e < kTileBytes / 16; e += 128)
+#pragma unroll 1
                             for (int c = 0; c < 4; c++) {
-                                const uint32_t m = E::wild(y[c]);
-                                y[c] &= ~((m & 0x8000u ? 0xFFFFu : 0u) | (m & 0x80000000u ? 0xFFFF0000u : 0u));
+                                const uint32_t m = E::wild(word[4 * e + c]);
+                                if (m & 0x8000u) word[4 * e + c] &= 0xFFFF0000u;
+                                if (m & 0x80000000u) word[4 * e + c] &= 0x0000FFFFu;
                             }
-                            reinterpret_cast<uint4 *>(v)[e] = make_uint4(y[0], y[1], y[2], y[3]);
-                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -427,14 +434,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 ring.next();  // V
             }
             wild = epilogue_any(wild);
+#pragma unroll 1
             for (int t = 0; t < sp.active && ok; t++) {
-                ok = __all_sync(kFull, mbar_wait_bounded(&sm.ml_full[t], done[t] & 1u));
+                ok = __all_sync(kFull, mbar_wait_short(&sm.ml_full[t], done[t] & 1u));
                 if (!ok) break;
                 const float2 ml = sm.ml[t][row];
                 const float inv = 1.0f / ml.y;
                 const int tok = u.tok0 + t * p.tile1_token + row / th, hq = u.h * G + t * p.tile1_head + row % th;
                 const bool live = row < th * tt && tok < u.n;
-                ok = __all_sync(kFull, mbar_wait_bounded(&sm.o_full[t], done[t] & 1u));
+                ok = __all_sync(kFull, mbar_wait_short(&sm.o_full[t], done[t] & 1u));
                 if (!ok) break;
                 done[t]++;
                 tc_fence_after();
@@ -446,18 +454,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     tmem_ld32_async(lane_tm + 256 * t + 128 + 64 * c, x[0]);
                     tmem_ld32_async(lane_tm + 256 * t + 128 + 64 * c + 32, x[1]);
                     tmem_ld_wait();
-                    if (wild && live) {
-                        // values that are not finite, of the keys this row sees in the mixed steps
-                        for (int j = sp.mixed * kKeys; j <= tok; j++) {
-                            const uint16_t *vr = p.v + (int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + 64 * c;
-#pragma unroll
-                            for (int e = 0; e < 64; e++) {
-                                const float y = E::value(vr[e]);
-                                uint32_t &z = x[e >> 5][e & 31];
-                                if (!(fabsf(y) < INFINITY)) z = __float_as_uint(__uint_as_float(z) + y);
-                            }
-                        }
-                    }
 #pragma unroll
                     for (int e = 0; e < 32; e++)
                         o[32 * c + e] = E::pack(__uint_as_float(x[e >> 4][2 * (e & 15)]) * inv,
@@ -472,6 +468,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 16; c++) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
                 if (p.lse) p.lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
+                if (wild) {  // what is not finite among the values this row sees in the mixed steps decides its element
+#pragma unroll 1
+                    for (int d = 0; d < kHeadDim; d++) {
+                        float y = 0.0f;
+#pragma unroll 1
+                        for (int j = sp.mixed * kKeys; j <= tok; j++) {
+                            const float x = E::value(p.v[(int64_t)(u.c0 + j) * p.v_stride + u.h * kHeadDim + d]);
+                            if (!(fabsf(x) < INFINITY)) y += x;
+                        }
+                        if (!(y == 0.0f)) p.out[at * kHeadDim + d] = (uint16_t)E::pack(y, 0.0f);
+                    }
+                }
             }
         }
     } else {
@@ -493,12 +501,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             auto wait_full = [&](uint32_t stage) {
                 const uint32_t parity = full_phase >> stage & 1u;
                 full_phase ^= 1u << stage;
-                return mbar_wait_bounded(&sm.kv_full[stage], parity);
+                return mbar_wait_short(&sm.kv_full[stage], parity);
             };
             auto wait_clean = [&](uint32_t stage) {
                 const uint32_t parity = clean_phase >> stage & 1u;
                 clean_phase ^= 1u << stage;
-                return mbar_wait_bounded(&sm.kv_clean[stage], parity);
+                return mbar_wait_short(&sm.kv_clean[stage], parity);
             };
             for (int r = 0; ok; r++) {
                 PromptUnit u;
@@ -524,10 +532,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     ring.next();
                 };
                 if (nst > 0) {
-                    ok = mbar_wait_bounded(&sm.q_full[t], uses & 1u) && wait_full(ring.stage);
+                    ok = mbar_wait_short(&sm.q_full[t], uses & 1u) && wait_full(ring.stage);
                     if (!ok) break;
                     issue_s(nst == 1, false);
-                    if (uses > 0) ok = mbar_wait_bounded(&sm.o_free[t], (uses - 1) & 1u);
+                    if (uses > 0) ok = mbar_wait_short(&sm.o_free[t], (uses - 1) & 1u);
                 } else {
                     ok = wait_full(ring.stage);
                     if (ok) mbar_arrive(&sm.kv_free[ring.stage]);
@@ -538,10 +546,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     // tiles take turns, so that one's softmax runs while the other's MMAs do
                     const bool live = i < nst, more = i + 1 < nst;
                     ok = i >= sp.mixed ? wait_clean(ring.stage) : wait_full(ring.stage);
-                    if (live) ok = ok && mbar_wait_bounded(&sm.p_full[t][0], p_phase);
+                    if (live) ok = ok && mbar_wait_short(&sm.p_full[t][0], p_phase);
                     const bool both = i < min(sp.steps[0], sp.steps[1]);
                     if (both) {
-                        ok = ok && mbar_wait_bounded(&sm.turn[t], turn_phase);
+                        ok = ok && mbar_wait_short(&sm.turn[t], turn_phase);
                         turn_phase ^= 1u;
                     }
                     if (!ok) break;
@@ -549,7 +557,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         const uint32_t c = v_lo + ring.stage * kStep;
 #pragma unroll
                         for (int x = 0; x < kParts; x++) {
-                            if (x > 0) ok = ok && mbar_wait_bounded(&sm.p_full[t][x], p_phase);
+                            if (x > 0) ok = ok && mbar_wait_short(&sm.p_full[t][x], p_phase);
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll
@@ -581,7 +589,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 uses += nst > 0;
             }
             umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
-            if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
+            if (!mbar_wait_short(&sm.mma_done, 0u)) ok = false;
         } else if (warp == 1) {
             // ---- units and copies ----
             const int H = p.num_heads, ut = p.unit_tokens;
@@ -595,16 +603,22 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const bool few = p.num_seqs <= 32;  // lengths stay in registers
             const int mine = few && lane < p.num_seqs ? length(lane) : 0;
             // sequences (of 32 from b0 on) with a unit number x, as a mask
-            auto longer = [&](int b0, int64_t x) {
+            auto longer = [&](int b0, int x) {
                 const int n = few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0;
-                return __ballot_sync(kFull, n > x * ut);
+                return __ballot_sync(kFull, n > (int64_t)x * ut);
             };
-            auto level = [&](int64_t x) {
+            auto level = [&](int x) {
                 int c = 0;
+#pragma unroll 1
                 for (int b0 = 0; b0 < p.num_seqs; b0 += 32) c += __popc(longer(b0, x));
                 return c;
             };
-            int64_t x = (p.max_n + ut - 1) / ut - 1, base = 0;  // units before level x
+            int longest = 0;
+#pragma unroll 1
+            for (int b0 = 0; b0 < p.num_seqs; b0 += 32)
+                longest = max(longest, few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0);
+            int x = (__reduce_max_sync(kFull, longest) + ut - 1) / ut - 1;
+            int64_t base = 0;  // units before level x
             int count = level(x);                                // sequences on level x
             Ring ring;
             uint32_t used = 0;  // stages filled so far, up to kStages
@@ -618,9 +632,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 PromptUnit u = {0, -1, 0, 0};
                 if (x >= 0) {
-                    const int64_t rank = id - base;
-                    int k = (int)(rank / H);  // the k-th sequence of the level
-                    u.h = (int)(rank % H);
+                    const uint32_t rank = (uint32_t)(id - base);  // (at most 65535 sequences x 65535 heads)
+                    int k = (int)(rank / (uint32_t)H);            // the k-th sequence of the level
+                    u.h = (int)(rank % (uint32_t)H);
+#pragma unroll 1
                     for (int b0 = 0;; b0 += 32) {
                         uint32_t m = longer(b0, x);
                         const int c = __popc(m);
@@ -628,14 +643,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                             k -= c;
                             continue;
                         }
-                        const int b = b0 + (int)__fns(m, 0, k + 1);
+#pragma unroll 1
+                        for (; k > 0; k--) m &= m - 1u;
+                        const int b = b0 + __ffs(m) - 1;
                         u.c0 = p.cu[b];
                         u.n = p.cu[b + 1] - u.c0;
                         break;
                     }
-                    u.tok0 = (int)(x * ut);
+                    u.tok0 = x * ut;
                 }
-                ok = __all_sync(kFull, r < 2 || mbar_wait_bounded(&sm.unit_free[r & 1], (uint32_t)((r >> 1) - 1) & 1u));
+                ok = __all_sync(kFull, r < 2 || mbar_wait_short(&sm.unit_free[r & 1], (uint32_t)((r >> 1) - 1) & 1u));
                 if (!ok) break;
                 if (lane == 0) {
                     sm.unit[r & 1] = u;
@@ -645,7 +662,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (lane == 0) {
                     const Span sp(u, p);
                     auto stage = [&](const CUtensorMap *map, int key, bool raw) {
-                        if (used >= kStages) ok = mbar_wait_bounded(&sm.kv_free[ring.stage], ring.phase ^ 1u);
+                        if (used >= kStages) ok = mbar_wait_short(&sm.kv_free[ring.stage], ring.phase ^ 1u);
                         if (!ok) return;
                         const uint32_t bit = 1u << ring.stage;
                         uint64_t *bar = raw ? &sm.kv_raw[ring.stage] : &sm.kv_full[ring.stage];
@@ -661,9 +678,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         if (used < kStages) used++;
                         ring.next();
                     };
+#pragma unroll 1
                     for (int i = 0; i < sp.total && ok; i++) {
-                        stage(&map_k, i * kKeys, false);
-                        if (ok) stage(&map_v, i * kKeys, i >= sp.mixed);
+#pragma unroll 1
+                        for (int kv = 0; kv < 2 && ok; kv++)
+                            stage(kv == 0 ? &map_k : &map_v, i * kKeys, kv == 1 && i >= sp.mixed);
                     }
                 }
                 ok = __all_sync(kFull, ok);
@@ -673,7 +692,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 for (uint32_t s = 0; s < used; s++) {
                     const bool raw = last_raw >> s & 1u;
                     const uint32_t next = (raw ? raw_phase : full_phase) >> s & 1u;
-                    if (!mbar_wait_bounded(raw ? &sm.kv_raw[s] : &sm.kv_full[s], next ^ 1u)) ok = false;
+                    if (!mbar_wait_short(raw ? &sm.kv_raw[s] : &sm.kv_full[s], next ^ 1u)) ok = false;
                 }
             }
         } else if (warp == 3 && lane == 0) {
@@ -688,7 +707,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
 #pragma unroll
                 for (int t = 0; t < kUnitTiles; t++) {
                     if (t >= sp.active || !ok) continue;
-                    if (uses[t] > 0) ok = mbar_wait_bounded(&sm.q_free[t], (uses[t] - 1) & 1u);
+                    if (uses[t] > 0) ok = mbar_wait_short(&sm.q_free[t], (uses[t] - 1) & 1u);
                     if (!ok) continue;
                     mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * th * tt);
                     const int tok = u.c0 + u.tok0 + t * p.tile1_token, hq = u.h * G + t * p.tile1_head;
@@ -698,7 +717,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
             }
             for (int t = 0; t < kUnitTiles; t++)  // no copy in flight when the CTA ends
-                if (uses[t] > 0 && !mbar_wait_bounded(&sm.q_full[t], (uses[t] - 1) & 1u)) ok = false;
+                if (uses[t] > 0 && !mbar_wait_short(&sm.q_full[t], (uses[t] - 1) & 1u)) ok = false;
         }
     }
     __syncwarp();

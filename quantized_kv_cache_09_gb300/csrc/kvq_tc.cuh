@@ -8,6 +8,19 @@
 
 namespace kvq {
 
+// mbar_wait_bounded in few instructions (a kernel of many roles waits in dozens of places, and
+// code that is run once a tile is fetched again each time when all of it does not fit the caches)
+__device__ __forceinline__ bool mbar_wait_short(uint64_t *bar, uint32_t parity)
+{
+    uint64_t t0 = 0;
+    while (!mbar_try_wait(bar, parity)) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) return false;
+    }
+    return true;
+}
+
 // matrix descriptor of a K-major tile (8-row x 128-byte atoms, 16-byte chunks XOR-ed with the
 // row): start address, 1024 bytes between 8-row groups, 128-byte swizzle
 __device__ __forceinline__ uint64_t umma_desc(uint32_t saddr)

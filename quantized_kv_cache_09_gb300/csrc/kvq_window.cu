@@ -6,14 +6,16 @@
 //
 // A persistent CTA per SM takes an equal contiguous share of all steps; a step is two pages (128
 // keys) of one (sequence, cache head, tile of 128 query rows).  Roles:
-//   warp 0       one thread issues the MMAs: S = Q K^T, M = N = 128, Q (two tiles) and three S in
-//                tensor memory (the lowest warp: the scheduler favours it, and all wait for it)
-//   warp 1       looks pages up and issues the bulk copies, five steps ahead
-//   warps 2-5    the next tile's query rows into tensor memory, a row per thread
-//   warps 6-9    widening: codes of a step from the copy ring to fp16 in shared memory (128-byte
+//   warps 0, 1   one thread each issues the MMAs of the even and of the odd steps: S = Q K^T, M = N
+//                = 128, Q (two tiles) and three S in tensor memory.  (A thread that has committed
+//                its MMAs gets nothing back from shared memory for some 500 cycles, even a
+//                barrier long complete: one thread for all steps took 1500 cycles a step.)
+//   warp 2       looks pages up and issues the bulk copies, five steps ahead
+//   warps 3-6    the next tile's query rows into tensor memory, a row per thread
+//   warps 7-10   widening: codes of a step from the copy ring to fp16 in shared memory (128-byte
 //                swizzled, K-major).  int4 pairs come out as elements (0,4) (1,5) (2,6) (3,7) of a
 //                word, and q is permuted alike
-//   warps 10-17  softmax sums, warps 10-13 the even steps, 14-17 the odd ones: one thread per query
+//   warps 11-18  softmax sums, warps 11-14 the even steps, 15-18 the odd ones: one thread per query
 //                row reads its 64 scores of each page from tensor memory
 // Every hand-off is an mbarrier, every wait bounded.  With 128 live rows a step costs about as
 // many cycles of the exponential unit (16384 / 32), of the tensor pipe (8 * 64) and of issue.
@@ -24,7 +26,7 @@ namespace kvq {
 
 namespace {
 
-constexpr int kWinThreads = 18 * 32;
+constexpr int kWinThreads = 19 * 32;
 constexpr int kWinRows = 128;
 constexpr int kWinKeys = 2 * kPage;
 constexpr int kCodeStages = 5, kKeyStages = 4, kScoreStages = 3, kMeta = 16;
@@ -37,7 +39,7 @@ constexpr uint32_t kWinIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) <<
 // what a step is: its sequence, cache head, first query row and page, key scales of its pages
 struct WinStep {
     int32_t c0, n, L, h, row0, j, pages;
-    int32_t first, last;  // of its tile's run in this CTA
+    int32_t tile, first, left;  // number of its tile in this CTA, whether it begins it, steps of it that follow
     float sk[2];
 };
 
@@ -131,9 +133,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(&sm.q_full[i], 4);
-            mbar_init(&sm.q_free[i], 1);
+            mbar_init(&sm.q_free[i], 2);
         }
-        mbar_init(&sm.mma_done, 1);
+        mbar_init(&sm.mma_done, 2);
         mbar_init_fence();
     }
     if (warp == 0) {
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     auto steps_of = [&](const PwSeq &s) { return (s.L + kWinKeys - 1) / kWinKeys; };
     auto tiles_of = [&](const PwSeq &s) { return (s.n * G + kWinRows - 1) / kWinRows; };
     bool bad_seq = false;
-    if (warp == 1) {
+    if (warp == 2) {
         int64_t run = 0;
         for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
             int64_t u = 0;
@@ -203,9 +205,9 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     const int steps = (int)(U * (blockIdx.x + 1) / gridDim.x - first);
     bool ok = true;
 
-    if (warp >= 6 && warp < 10) {
+    if (warp >= 7 && warp < 11) {
         // ---- widening ----
-        const int wt = tid - 6 * 32;
+        const int wt = tid - 7 * 32;
         Turn<kCodeStages> code;
         Turn<kKeyStages> key;
         for (int i = 0; i < steps; i++, code.next(), key.next()) {
@@ -251,13 +253,13 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 mbar_arrive(&sm.code_free[code.stage]);
             }
         }
-    } else if (warp >= 10) {
+    } else if (warp >= 11) {
         // ---- softmax sums: one query row per thread ----
         const int row = (warp & 3) * 32 + lane;
         const float sabs = fmaxf(fabsf(p.score_scale), kPwMinScale);
         Turn<kScoreStages> score;
         for (int i = 0; i < steps; i++, score.next()) {
-            if ((i & 1) != (warp - 10) >> 2) continue;
+            if ((i & 1) != (warp - 11) >> 2) continue;
             const uint32_t ss = score.stage;
             ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[ss], score.parity));
             if (!ok) break;
@@ -308,37 +310,40 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 if (hh < m.pages && rr < m.n * G) dst[hh] = f * mx + __log2f(la + lb);
             }
         }
-    } else if (warp == 0) {
+    } else if (warp < 2) {
         if (lane == 0) {
-            // ---- the MMA thread ----
+            // ---- an MMA thread: steps warp, warp + 2, ... ----
             const uint32_t hi = (uint32_t)(umma_desc(smem_addr(sm.k[0])) >> 32);
             const uint32_t k_lo = (uint32_t)umma_desc(smem_addr(sm.k[0]));
             Turn<kKeyStages> key;
             Turn<kScoreStages> score;
-            Turn<2> query;
+            int have = -1;  // the query tile that was waited for
             for (int i = 0; i < steps && ok; i++, key.next(), score.next()) {
+                if ((i & 1) != warp) continue;
                 ok = mbar_wait_bounded(&sm.k_full[key.stage], key.parity);
-                if (ok && sm.meta[i % kMeta].first) ok = mbar_wait_bounded(&sm.q_full[query.stage], query.parity);
+                if (!ok) break;
+                const int tile = sm.meta[i % kMeta].tile, first = sm.meta[i % kMeta].first, left = sm.meta[i % kMeta].left;
+                if (tile != have) ok = mbar_wait_bounded(&sm.q_full[tile & 1], (uint32_t)(tile >> 1) & 1u);
+                have = tile;
                 if (ok && i >= kScoreStages) ok = mbar_wait_bounded(&sm.s_free[score.stage], score.parity ^ 1u);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t b = k_lo + key.stage * (kWinTile >> 4), a = tmem + 384 + 64 * query.stage;
+                const uint32_t b = k_lo + key.stage * (kWinTile >> 4), a = tmem + 384 + 64 * (tile & 1);
 #pragma unroll
                 for (int k = 0; k < 8; k++)
                     umma_f16_ts(tmem + 128 * score.stage, a + 8 * k,
                                 b + (uint32_t)(((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4), hi, kWinIdesc,
                                 k > 0 ? 1u : 0u);
+                // both threads let a tile go after their last step of it (one for both where it has one step)
+                if (left <= 1) umma_commit(&sm.q_free[tile & 1]);
+                if (left == 0 && first) umma_commit(&sm.q_free[tile & 1]);
                 umma_commit(&sm.s_full[score.stage]);
                 umma_commit(&sm.k_free[key.stage]);
-                if (sm.meta[i % kMeta].last) {
-                    umma_commit(&sm.q_free[query.stage]);
-                    query.next();
-                }
             }
             umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
             if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
         }
-    } else if (warp == 1) {
+    } else if (warp == 2) {
         // ---- pages and copies: lane l looks up step l of 32, two rings in turn ----
         WinStep ring[2];
         uint32_t ph[2][2];
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             int k, all;
             const int b = place(first + i + lane, m, k, all);
             m.first = k == 0 || i + lane == 0;
-            m.last = k == all - 1 || i + lane == steps - 1;
+            m.left = min(all - 1 - k, steps - 1 - (i + lane));
 #pragma unroll
             for (int x = 0; x < 2; x++) {
                 at[x] = 0;
@@ -365,7 +370,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
         look(0, ring[0], ph[0]);
         look(32, ring[1], ph[1]);
         Turn<kCodeStages> code;
-        int used = 0;
+        int used = 0, tile = -1;
         for (int i = 0; i < steps; i++, code.next()) {
             if (i > 0 && (i & 31) == 0) {
                 if (i & 32)
@@ -375,8 +380,10 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             }
             if (i >= kCodeStages) ok = __all_sync(kFull, mbar_wait_bounded(&sm.code_free[code.stage], code.parity ^ 1u));
             if (!ok) break;
-            auto issue = [&](const WinStep &m, const uint32_t (&at)[2]) {
+            auto issue = [&](WinStep &m, const uint32_t (&at)[2]) {
+                tile += __shfl_sync(kFull, m.first, i & 31);
                 if (lane == (i & 31)) {
+                    m.tile = tile;
                     sm.meta[i % kMeta] = m;
                     uint64_t *bar = &sm.code_full[code.stage];
                     mbar_arrive_expect_tx(bar, m.pages * kPageBytes);
