@@ -24,7 +24,7 @@
 //             lower warps, and these few instructions are the ones that others
 //             wait for: behind the softmax they were late by hundreds of cycles.)
 //   1         walks the unit list and issues the copies of K and V (TMA) into a
-//             ring of five 32 KB stages.
+//             ring of four 32 KB stages.
 //   3         issues the copies of the Q tiles.
 //   4-7, 8-11 softmax of tile 0, tile 1: one thread per query row.  A row of S
 //             (128 scores) is read into registers once; maximum, 2^(s - m), the
@@ -58,7 +58,8 @@ namespace {
 constexpr int kTileRows = 128;
 constexpr int kUnitTiles = 2;
 constexpr int kKeys = 128;
-constexpr int kStages = 5;
+constexpr int kStages = 4;
+constexpr int kOutPitch = 144;  // bytes: 128 and a step of 16 that keeps the rows' banks apart
 constexpr int kParts = 3;  // P is handed over as keys 0..63, 64..95, 96..127
 constexpr int kTileBytes = kTileRows * kHeadDim * 2;
 constexpr int kPromptThreads = 512;
@@ -111,6 +112,7 @@ struct PromptUnit {
 struct alignas(1024) PromptSmem {
     uint8_t q[kUnitTiles][kTileBytes];
     uint8_t kv[kStages][kTileBytes];
+    uint8_t o[4][32 * kOutPitch];  // by epilogue warp: 64 elements of its 32 rows on their way out
     uint64_t kv_full[kStages];   // a stage's copy done: K, or V of a step without masked keys
     uint64_t kv_raw[kStages];    // the same for V of a mixed step (then kv_clean)
     uint64_t kv_clean[kStages];  // that V cleaned
@@ -463,11 +465,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.o_free[t]);
-                if (!live) continue;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * kHeadDim);
+                // The rows leave through shared memory, 4 of 128 bytes an instruction: 16 bytes a lane of 32
+                // rows straight from registers hold up every other warp's shared-memory access.
+                const int64_t at0 = (int64_t)(u.c0 + u.tok0) * p.num_q_heads + u.h * G;
+                const int rel = live ? (int)(at - at0) : -1;
+                uint8_t *stage = sm.o[warp & 3];
 #pragma unroll
-                for (int c = 0; c < 16; c++) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+                for (int half = 0; half < 2; half++) {
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; c++)
+                        *reinterpret_cast<uint4 *>(stage + lane * kOutPitch + 16 * c) =
+                            make_uint4(o[32 * half + 4 * c], o[32 * half + 4 * c + 1], o[32 * half + 4 * c + 2],
+                                       o[32 * half + 4 * c + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        const int to = __shfl_sync(kFull, rel, 4 * k + (lane >> 3));
+                        const uint4 x =
+                            *reinterpret_cast<const uint4 *>(stage + (4 * k + (lane >> 3)) * kOutPitch + 16 * (lane & 7));
+                        if (to >= 0)
+                            *reinterpret_cast<uint4 *>(p.out + (at0 + to) * kHeadDim + 64 * half + 8 * (lane & 7)) = x;
+                    }
+                }
+                __syncwarp();
+                if (!live) continue;
                 if (p.lse) p.lse[at] = (ml.x + __log2f(ml.y)) * kLn2;
+                // (the lanes that stored this row did so before the barrier)
                 if (wild) {  // what is not finite among the values this row sees in the mixed steps decides its element
 #pragma unroll 1
                     for (int d = 0; d < kHeadDim; d++) {
