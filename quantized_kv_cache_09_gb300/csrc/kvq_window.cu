@@ -7,15 +7,17 @@
 // A persistent CTA per SM takes an equal contiguous share of all steps; a step is two pages (128
 // keys) of one (sequence, cache head, tile of 128 query rows).  Roles:
 //   warps 0, 1   one thread each issues the MMAs of the even and of the odd steps: S = Q K^T, M = N
-//                = 128, Q (two tiles) and three S in tensor memory.  (A thread that has committed
+//                = 128, Q (two tiles) and two S in tensor memory.  (A thread that has committed
 //                its MMAs gets nothing back from shared memory for some 500 cycles, even a
 //                barrier long complete: one thread for all steps took 1500 cycles a step.)
-//   warp 2       looks pages up and issues the bulk copies, five steps ahead
-//   warps 3-6    the next tile's query rows into tensor memory, a row per thread
-//   warps 7-10   widening: codes of a step from the copy ring to fp16 in shared memory (128-byte
+//   warps 2, 3   look pages up and issue the bulk copies of the even and of the odd steps, up to
+//                four steps ahead (a copy of 8 KB holds its issuer ~450 cycles: one warp took
+//                1450 cycles a step)
+//   warps 4-7    the next tile's query rows into tensor memory, a row per thread
+//   warps 8-11   widening: codes of a step from the copy ring to fp16 in shared memory (128-byte
 //                swizzled, K-major).  int4 pairs come out as elements (0,4) (1,5) (2,6) (3,7) of a
 //                word, and q is permuted alike
-//   warps 11-18  softmax sums, warps 11-14 the even steps, 15-18 the odd ones: one thread per query
+//   warps 12-19  softmax sums, warps 12-15 the even steps, 16-19 the odd ones: one thread per query
 //                row reads its 64 scores of each page from tensor memory
 // Every hand-off is an mbarrier, every wait bounded.  With 128 live rows a step costs about as
 // many cycles of the exponential unit (16384 / 32), of the tensor pipe (8 * 64) and of issue.
@@ -26,14 +28,18 @@ namespace kvq {
 
 namespace {
 
-constexpr int kWinThreads = 19 * 32;
+constexpr int kWinThreads = 20 * 32;
 constexpr int kWinRows = 128;
 constexpr int kWinKeys = 2 * kPage;
-constexpr int kCodeStages = 5, kKeyStages = 4, kScoreStages = 3, kMeta = 16;
+// Even numbers of stages: the even and the odd steps have their own copy warp, MMA thread and
+// softmax warps, which run ahead of one another, so each keeps to its own stages (a wait by parity
+// of a stage that both used would take the use before last for the last).
+constexpr int kCodeStages = 4, kKeyStages = 4, kScoreStages = 2, kMeta = 16;
+static_assert(kCodeStages % 2 == 0 && kKeyStages % 2 == 0 && kScoreStages % 2 == 0, "stages by parity of the step");
 // a step's record lives until its sums are done: the copies run at most the sum of the stages ahead
 static_assert(kMeta >= kCodeStages + kKeyStages + kScoreStages + 2, "records outlive their steps");
 constexpr int kWinTile = kWinKeys * kHeadDim * 2;
-constexpr uint32_t kWinTmem = 512;    // S at columns 128 * stage, Q at 384 + 64 * buffer
+constexpr uint32_t kWinTmem = 512;    // S at columns 128 * stage, Q at 256 + 64 * buffer
 constexpr uint32_t kWinIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);  // f32 += f16 x f16, M = N = 128
 
 // what a step is: its sequence, cache head, first query row and page, key scales of its pages
@@ -205,13 +211,13 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
     const int steps = (int)(U * (blockIdx.x + 1) / gridDim.x - first);
     bool ok = true;
 
-    if (warp >= 7 && warp < 11) {
+    if (warp >= 8 && warp < 12) {
         // ---- widening ----
-        const int wt = tid - 7 * 32;
+        const int wt = tid - 8 * 32;
         Turn<kCodeStages> code;
         Turn<kKeyStages> key;
         for (int i = 0; i < steps; i++, code.next(), key.next()) {
-            ok = mbar_wait_bounded(&sm.code_full[code.stage], code.parity);
+            ok = mbar_wait_short(&sm.code_full[code.stage], code.parity);
             constexpr int kLd = 2 * kPageBytes / (16 * 128);  // 16-byte pieces per thread
             // int4: 8 threads take 4 keys x 2 pieces (16 bytes of a row), else 2 keys x 4 pieces: the
             // stores meet no bank conflict
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             uint4 w[kLd];
 #pragma unroll
             for (int r = 0; r < kLd; r++) w[r] = *reinterpret_cast<const uint4 *>(sm.code[code.stage] + key_of(r) * RB + 16 * piece_of(r));
-            if (ok && i >= kKeyStages) ok = mbar_wait_bounded(&sm.k_free[key.stage], key.parity ^ 1u);
+            if (ok && i >= kKeyStages) ok = mbar_wait_short(&sm.k_free[key.stage], key.parity ^ 1u);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
             uint8_t *dst = sm.k[key.stage];
@@ -253,15 +259,15 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 mbar_arrive(&sm.code_free[code.stage]);
             }
         }
-    } else if (warp >= 11) {
+    } else if (warp >= 12) {
         // ---- softmax sums: one query row per thread ----
         const int row = (warp & 3) * 32 + lane;
         const float sabs = fmaxf(fabsf(p.score_scale), kPwMinScale);
         Turn<kScoreStages> score;
         for (int i = 0; i < steps; i++, score.next()) {
-            if ((i & 1) != (warp - 11) >> 2) continue;
+            if ((i & 1) != (warp - 12) >> 2) continue;
             const uint32_t ss = score.stage;
-            ok = __all_sync(kFull, mbar_wait_bounded(&sm.s_full[ss], score.parity));
+            ok = __all_sync(kFull, mbar_wait_short(&sm.s_full[ss], score.parity));
             if (!ok) break;
             tc_fence_after();
             const WinStep m = sm.meta[i % kMeta];
@@ -320,15 +326,15 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             int have = -1;  // the query tile that was waited for
             for (int i = 0; i < steps && ok; i++, key.next(), score.next()) {
                 if ((i & 1) != warp) continue;
-                ok = mbar_wait_bounded(&sm.k_full[key.stage], key.parity);
+                ok = mbar_wait_short(&sm.k_full[key.stage], key.parity);
                 if (!ok) break;
                 const int tile = sm.meta[i % kMeta].tile, first = sm.meta[i % kMeta].first, left = sm.meta[i % kMeta].left;
-                if (tile != have) ok = mbar_wait_bounded(&sm.q_full[tile & 1], (uint32_t)(tile >> 1) & 1u);
+                if (tile != have) ok = mbar_wait_short(&sm.q_full[tile & 1], (uint32_t)(tile >> 1) & 1u);
                 have = tile;
-                if (ok && i >= kScoreStages) ok = mbar_wait_bounded(&sm.s_free[score.stage], score.parity ^ 1u);
+                if (ok && i >= kScoreStages) ok = mbar_wait_short(&sm.s_free[score.stage], score.parity ^ 1u);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t b = k_lo + key.stage * (kWinTile >> 4), a = tmem + 384 + 64 * (tile & 1);
+                const uint32_t b = k_lo + key.stage * (kWinTile >> 4), a = tmem + 256 + 64 * (tile & 1);
 #pragma unroll
                 for (int k = 0; k < 8; k++)
                     umma_f16_ts(tmem + 128 * score.stage, a + 8 * k,
@@ -341,10 +347,10 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 umma_commit(&sm.k_free[key.stage]);
             }
             umma_commit(&sm.mma_done);  // whatever was issued completes before tensor memory is freed
-            if (!mbar_wait_bounded(&sm.mma_done, 0u)) ok = false;
+            if (!mbar_wait_short(&sm.mma_done, 0u)) ok = false;
         }
-    } else if (warp == 2) {
-        // ---- pages and copies: lane l looks up step l of 32, two rings in turn ----
+    } else if (warp < 4) {
+        // ---- pages and copies of steps warp - 2, warp, ...: lane l looks up step l of 32, two rings in turn ----
         WinStep ring[2];
         uint32_t ph[2][2];
         auto look = [&](int i, WinStep &m, uint32_t (&at)[2]) {
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
         look(0, ring[0], ph[0]);
         look(32, ring[1], ph[1]);
         Turn<kCodeStages> code;
-        int used = 0, tile = -1;
+        int tile = -1, mine = 0;  // steps copied here
         for (int i = 0; i < steps; i++, code.next()) {
             if (i > 0 && (i & 31) == 0) {
                 if (i & 32)
@@ -378,29 +384,32 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 else
                     look(i + 32, ring[1], ph[1]);
             }
-            if (i >= kCodeStages) ok = __all_sync(kFull, mbar_wait_bounded(&sm.code_free[code.stage], code.parity ^ 1u));
+            tile += i & 32 ? __shfl_sync(kFull, ring[1].first, i & 31) : __shfl_sync(kFull, ring[0].first, i & 31);
+            if ((i & 1) != (warp & 1)) continue;
+            if (i >= kCodeStages) ok = __all_sync(kFull, mbar_wait_short(&sm.code_free[code.stage], code.parity ^ 1u));
             if (!ok) break;
             auto issue = [&](WinStep &m, const uint32_t (&at)[2]) {
-                tile += __shfl_sync(kFull, m.first, i & 31);
                 if (lane == (i & 31)) {
                     m.tile = tile;
                     sm.meta[i % kMeta] = m;
                     uint64_t *bar = &sm.code_full[code.stage];
                     mbar_arrive_expect_tx(bar, m.pages * kPageBytes);
-                    for (int x = 0; x < m.pages; x++)
-                        bulk_copy_g2s(sm.code[code.stage] + x * kPageBytes, p.k_codes + (size_t)at[x] * kPageBytes,
-                                      kPageBytes, bar);
+#pragma unroll
+                    for (int x = 0; x < 2; x++)
+                        if (x < m.pages)
+                            bulk_copy_g2s(sm.code[code.stage] + x * kPageBytes, p.k_codes + (size_t)at[x] * kPageBytes,
+                                          kPageBytes, bar);
                 }
             };
             if (i & 32)
                 issue(ring[1], ph[1]);
             else
                 issue(ring[0], ph[0]);
-            used = i + 1;
+            mine = i + 1;
         }
         // no copy in flight when the CTA ends
-        for (int i = max(0, used - kCodeStages); i < used; i++)
-            if (!mbar_wait_bounded(&sm.code_full[i % kCodeStages], (uint32_t)(i / kCodeStages) & 1u)) ok = false;
+        for (int i = mine - 1; i >= 0 && i > mine - 1 - kCodeStages; i -= 2)
+            if (!mbar_wait_short(&sm.code_full[i % kCodeStages], (uint32_t)(i / kCodeStages) & 1u)) ok = false;
     } else {
         // ---- query rows ----
         const int row = (warp & 3) * 32 + lane;
@@ -426,11 +435,11 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 for (int e = 0; e < 4; e++)
                     x[c >> 3][4 * (c & 7) + e] = h2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&y[e]), flip));
             }
-            if (tiles >= 2) ok = mbar_wait_bounded(&sm.q_free[query.stage], query.parity ^ 1u);
+            if (tiles >= 2) ok = mbar_wait_short(&sm.q_free[query.stage], query.parity ^ 1u);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t tm = tmem + 384 + 64 * query.stage + ((uint32_t)((warp & 3) * 32) << 16);
+            const uint32_t tm = tmem + 256 + 64 * query.stage + ((uint32_t)((warp & 3) * 32) << 16);
             tmem_st32(tm, x[0]);
             tmem_st32(tm + 32, x[1]);
             tmem_st_wait();
