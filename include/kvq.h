@@ -383,8 +383,9 @@ kvq_status kvq_prompt_attention(kvq_dtype dtype, const uint16_t *q, int64_t q_ro
  * A sequence that breaks a bound is skipped (its row stays as it was) and
  * KVQ_FLAG_BAD_LENGTH set; a block-table entry out of range sets
  * KVQ_FLAG_BAD_PAGE (page 0 is read instead).  Errors: KVQ_ERR_INVALID_ARG,
- * KVQ_ERR_UNSUPPORTED (also max_blocks_per_seq above 2^22, or 2^30 or more
- * query rows of one sequence and cache head), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
+ * KVQ_ERR_UNSUPPORTED (also max_blocks_per_seq above 2^22, 2^30 or more
+ * query rows of one sequence and cache head, or more than 2^31 pages x cache
+ * heads x blocks of query rows of one sequence, 8 or, above 16, 128 rows a block), KVQ_ERR_WORKSPACE, KVQ_ERR_CUDA.
  */
 kvq_status kvq_page_weights(const kvq_cache *cache, const uint16_t *q, int32_t num_q_heads,
                             const int32_t *cu_seqlens_q, int64_t total_q, int32_t max_q_per_seq,

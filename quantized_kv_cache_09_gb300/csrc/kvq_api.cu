@@ -328,6 +328,10 @@ kvq_status kvq_page_weights(const kvq_cache *cache, const uint16_t *q, int32_t n
     if (num_q_heads <= 0 || num_q_heads % cache->num_heads) return KVQ_ERR_INVALID_ARG;
     const int g = num_q_heads / cache->num_heads;
     if (max_blocks_per_seq > (1 << 22) || (int64_t)max_q_per_seq * g >= (1 << 30)) return KVQ_ERR_UNSUPPORTED;
+    // the units (pages of a cache head and block of query rows) of one sequence are counted in 31 bits
+    const int64_t rows = (int64_t)max_q_per_seq * g;
+    const int64_t blocks = rows <= 16 ? (rows + 7) / 8 : (rows + 127) / 128;
+    if ((double)max_blocks_per_seq * cache->num_heads * (double)blocks > INT32_MAX) return KVQ_ERR_UNSUPPORTED;
     if (num_seqs == 0) return KVQ_OK;
     if (!cu_seqlens_q || !block_table || !seq_lens || !weights_out) return KVQ_ERR_INVALID_ARG;
     if (total_q > 0 && max_q_per_seq > 0) {

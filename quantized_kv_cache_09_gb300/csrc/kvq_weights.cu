@@ -152,10 +152,10 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
         x.b = lo;
         pw_seq(p, lo, x.s);
         const int np = (x.s.L + kPage - 1) / kPage, blocks = (x.s.n * G + kCols - 1) / kCols;
-        const int64_t r = u - sm.upto[lo], hr = r / np;
-        x.j = (int)(r - hr * np);
-        x.h = (int)(hr / blocks);
-        x.row0 = (int)(hr % blocks) * kCols;
+        const uint32_t r = (uint32_t)(u - sm.upto[lo]), hr = r / (uint32_t)np;  // (under 2^31 of one sequence)
+        x.j = (int)(r - hr * (uint32_t)np);
+        x.h = (int)(hr / (uint32_t)blocks);
+        x.row0 = (int)(hr % (uint32_t)blocks) * kCols;
         return x;
     };
 

@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
         pw_seq(p, lo, s);
         all = steps_of(s);
         const int tiles = tiles_of(s);
-        const int64_t r = u - sm.upto[lo], hr = r / all;
-        k = (int)(r - hr * all);
+        const uint32_t r = (uint32_t)(u - sm.upto[lo]), hr = r / (uint32_t)all;  // (under 2^31 of one sequence)
+        k = (int)(r - hr * (uint32_t)all);
         m.c0 = s.c0;
         m.n = s.n;
         m.L = s.L;
-        m.h = (int)(hr / tiles);
-        m.row0 = (int)(hr % tiles) * kWinRows;
+        m.h = (int)(hr / (uint32_t)tiles);
+        m.row0 = (int)(hr % (uint32_t)tiles) * kWinRows;
         m.j = 2 * k;
         m.pages = min(2, (s.L + kPage - 1) / kPage - m.j);
         return lo;
@@ -370,19 +370,18 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                     pg = 0;
                 }
                 at[x] = (uint32_t)pg * (uint32_t)H + (uint32_t)m.h;
-                m.sk[x] = p.k_scales[at[x]];
+                m.sk[x] = p.k_scales[at[x]];  // (not waited for: the copies come first)
             }
         };
         look(0, ring[0], ph[0]);
-        look(32, ring[1], ph[1]);
         Turn<kCodeStages> code;
         int tile = -1, mine = 0;  // steps copied here
         for (int i = 0; i < steps; i++, code.next()) {
-            if (i > 0 && (i & 31) == 0) {
+            if ((i & 31) == kCodeStages) {  // (once the stages are filled)
                 if (i & 32)
-                    look(i + 32, ring[0], ph[0]);
+                    look(i - kCodeStages + 32, ring[0], ph[0]);
                 else
-                    look(i + 32, ring[1], ph[1]);
+                    look(i - kCodeStages + 32, ring[1], ph[1]);
             }
             tile += i & 32 ? __shfl_sync(kFull, ring[1].first, i & 31) : __shfl_sync(kFull, ring[0].first, i & 31);
             if ((i & 1) != (warp & 1)) continue;
@@ -390,15 +389,15 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             if (!ok) break;
             auto issue = [&](WinStep &m, const uint32_t (&at)[2]) {
                 if (lane == (i & 31)) {
-                    m.tile = tile;
-                    sm.meta[i % kMeta] = m;
                     uint64_t *bar = &sm.code_full[code.stage];
-                    mbar_arrive_expect_tx(bar, m.pages * kPageBytes);
 #pragma unroll
                     for (int x = 0; x < 2; x++)
                         if (x < m.pages)
                             bulk_copy_g2s(sm.code[code.stage] + x * kPageBytes, p.k_codes + (size_t)at[x] * kPageBytes,
                                           kPageBytes, bar);
+                    m.tile = tile;
+                    sm.meta[i % kMeta] = m;  // (the phase is not over before the arrival, whatever has come)
+                    mbar_arrive_expect_tx(bar, m.pages * kPageBytes);
                 }
             };
             if (i & 32)

@@ -59,6 +59,7 @@ def test_page_weights_refusals():
     assert call(n=-1) == 1 and call(mx=-1) == 1 and call(total=-1) == 1 and call(mb=0) == 1
     assert call(scale=math.nan) == 1 and call(decay=math.inf) == 1 and call(hq=3) == 1 and call(hq=0) == 1
     assert call(mb=(1 << 22) + 1) == 2 and call(mx=1 << 28) == 2
+    assert call(mb=1 << 22, mx=1 << 20, total=1) == 2                        # units of one sequence
     assert call(n=0, q=None, cu=None, bt=None, lens=None, wout=None, ws=None) == 0
     for name in ("q", "cu", "bt", "lens", "wout"):
         assert call(**{name: None}) == 1, name
