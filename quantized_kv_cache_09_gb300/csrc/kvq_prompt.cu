@@ -39,9 +39,12 @@
 //             epilogue: O / l, while the tensor cores are on the next unit.
 // While one tile's rows are in the softmax, the tensor cores work on the other.
 //
-// Unit order: by the number of the unit in its sequence, the highest (most
-// keys) first, over sequences and cache heads, dealt to the CTAs forwards and
-// backwards in turn -- longest first without a counter to fetch from.
+// Unit order: cache heads in groups whose keys and values fit half of L2 (each
+// level reads them again: 8 x 2048 x 32 heads without groups read 1.2 GB from
+// HBM for 268 MB of keys and values); of a group by the number of the unit in
+// its sequence, the highest (most keys) first, over sequences and heads, dealt
+// to the CTAs forwards and backwards in turn -- longest first without a counter
+// to fetch from.
 #include <cuda.h>
 
 #include <type_traits>
@@ -62,6 +65,7 @@ constexpr int kStages = 4;
 constexpr int kOutPitch = 144;  // bytes: 128 and a step of 16 that keeps the rows' banks apart
 constexpr int kParts = 3;  // P is handed over as keys 0..63, 64..95, 96..127
 constexpr int kTileBytes = kTileRows * kHeadDim * 2;
+constexpr int64_t kGroupBytes = 64 << 20;  // half of L2
 constexpr int kPromptThreads = 512;
 constexpr uint32_t kPromptTmem = 512;  // tile t: S / P at columns 256 t, O at 256 t + 128
 constexpr float kLazy = 8.0f;
@@ -541,9 +545,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 const int nst = t == 0 ? sp.steps[0] : sp.steps[1];
                 // S of a step goes over P of the step before, whose PV was issued before it: the
                 // tensor pipe runs one thread's MMAs in order
-                auto issue_s = [&](bool last, bool pass) {
-                    tc_fence_after();
-                    const uint32_t b = k_lo + ring.stage * kStep;
+                auto issue_s = [&](uint32_t stage, bool pass) {
+                    const uint32_t b = k_lo + stage * kStep;
 #pragma unroll
                     for (int ks = 0; ks < 8; ks++) {
                         const uint32_t d = (uint32_t)(((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) >> 4);
@@ -551,14 +554,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         if (ks == 4 && pass) mbar_arrive(&sm.turn[t ^ 1]);  // the pipe is fed while it wakes
                     }
                     umma_commit(&sm.s_full[t]);
-                    umma_commit(&sm.kv_free[ring.stage]);
-                    if (last) umma_commit(&sm.q_free[t]);
-                    ring.next();
                 };
                 if (nst > 0) {
                     ok = mbar_wait_short(&sm.q_full[t], uses & 1u) && wait_full(ring.stage);
                     if (!ok) break;
-                    issue_s(nst == 1, false);
+                    tc_fence_after();
+                    issue_s(ring.stage, false);
+                    umma_commit(&sm.kv_free[ring.stage]);
+                    if (nst == 1) umma_commit(&sm.q_free[t]);
+                    ring.next();
                     if (uses > 0) ok = mbar_wait_short(&sm.o_free[t], (uses - 1) & 1u);
                 } else {
                     ok = wait_full(ring.stage);
@@ -569,7 +573,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     // O += P(i) V(i), in the parts that the softmax hands over, then S(i + 1); the
                     // tiles take turns, so that one's softmax runs while the other's MMAs do
                     const bool live = i < nst, more = i + 1 < nst;
-                    ok = i >= sp.mixed ? wait_clean(ring.stage) : wait_full(ring.stage);
+                    const uint32_t stage_v = ring.stage;
+                    ring.next();
+                    ok = i >= sp.mixed ? wait_clean(stage_v) : wait_full(stage_v);
+                    // (the next K's wait ahead of the turn: nothing comes between this PV and the next S)
+                    if (i + 1 < sp.total) ok = ok && wait_full(ring.stage);
                     if (live) ok = ok && mbar_wait_short(&sm.p_full[t][0], p_phase);
                     const bool both = i < min(sp.steps[0], sp.steps[1]);
                     if (both) {
@@ -578,7 +586,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     }
                     if (!ok) break;
                     if (live) {
-                        const uint32_t c = v_lo + ring.stage * kStep;
+                        const uint32_t c = v_lo + stage_v * kStep;
 #pragma unroll
                         for (int x = 0; x < kParts; x++) {
                             if (x > 0) ok = ok && mbar_wait_short(&sm.p_full[t][x], p_phase);
@@ -591,24 +599,23 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         }
                         if (!ok) break;
                         p_phase ^= 1u;
-                        umma_commit(&sm.kv_free[ring.stage]);
-                        if (!more) umma_commit(&sm.o_full[t]);
+                        if (more)
+                            issue_s(ring.stage, both);
+                        else
+                            umma_commit(&sm.o_full[t]);
+                        umma_commit(&sm.kv_free[stage_v]);
                     } else {
-                        mbar_arrive(&sm.kv_free[ring.stage]);
+                        mbar_arrive(&sm.kv_free[stage_v]);
                     }
-                    ring.next();
-                    if (more) {
-                        ok = wait_full(ring.stage);
-                        if (!ok) break;
-                        issue_s(i + 2 == nst, both);
-                    } else {
-                        if (both) mbar_arrive(&sm.turn[t ^ 1]);
-                        if (i + 1 < sp.total) {  // the other tile's K: seen, so that the phases stay in step
-                            ok = wait_full(ring.stage);
-                            if (ok) mbar_arrive(&sm.kv_free[ring.stage]);
-                            ring.next();
-                        }
+                    if (both && !more) mbar_arrive(&sm.turn[t ^ 1]);
+                    if (i + 1 < sp.total) {
+                        if (more)
+                            umma_commit(&sm.kv_free[ring.stage]);
+                        else  // the other tile's K, seen so that the phases stay in step
+                            mbar_arrive(&sm.kv_free[ring.stage]);
+                        ring.next();
                     }
+                    if (i + 2 == nst) umma_commit(&sm.q_free[t]);
                 }
                 uses += nst > 0;
             }
@@ -638,27 +645,42 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 return c;
             };
             int longest = 0;
+            int64_t tokens = 0;
 #pragma unroll 1
-            for (int b0 = 0; b0 < p.num_seqs; b0 += 32)
-                longest = max(longest, few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0);
-            int x = (__reduce_max_sync(kFull, longest) + ut - 1) / ut - 1;
-            int64_t base = 0;  // units before level x
-            int count = level(x);                                // sequences on level x
+            for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+                const int n = few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0;
+                longest = max(longest, n);
+                tokens += n;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(kFull, tokens, o);
+            const int top = (__reduce_max_sync(kFull, longest) + ut - 1) / ut - 1;
+            // heads go in groups whose K and V stay in L2 while all levels read them
+            const int64_t groups = (tokens * H * (kHeadDim * 4) + kGroupBytes - 1) / kGroupBytes;
+            const int hg = groups > H ? 1 : groups > 1 ? (int)((H + groups - 1) / groups) : H;
+            int x = top, h0 = top < 0 ? H : 0, hn = hg;
+            int64_t base = 0;      // units before level x of the heads from h0 on
+            int count = level(x);  // sequences on level x
             Ring ring;
             uint32_t used = 0;  // stages filled so far, up to kStages
             // bit s: parity of stage s's next kv_full, kv_raw; whether its last fill was a mixed V
             uint32_t full_phase = 0, raw_phase = 0, last_raw = 0;
             for (int r = 0;; r++) {
                 const int64_t id = (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                while (x >= 0 && id >= base + (int64_t)count * H) {
-                    base += (int64_t)count * H;
-                    if (--x >= 0) count = level(x);
+                while (h0 < H && id >= base + (int64_t)count * hn) {
+                    base += (int64_t)count * hn;
+                    if (--x < 0) {
+                        h0 += hg;
+                        hn = min(hg, H - h0);
+                        x = top;
+                    }
+                    count = level(x);
                 }
                 PromptUnit u = {0, -1, 0, 0};
-                if (x >= 0) {
+                if (h0 < H) {
                     const uint32_t rank = (uint32_t)(id - base);  // (at most 65535 sequences x 65535 heads)
-                    int k = (int)(rank / (uint32_t)H);            // the k-th sequence of the level
-                    u.h = (int)(rank % (uint32_t)H);
+                    int k = (int)(rank / (uint32_t)hn);           // the k-th sequence of the level
+                    u.h = h0 + (int)(rank % (uint32_t)hn);
 #pragma unroll 1
                     for (int b0 = 0;; b0 += 32) {
                         uint32_t m = longer(b0, x);
