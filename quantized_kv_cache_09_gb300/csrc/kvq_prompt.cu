@@ -453,22 +453,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 done[t]++;
                 tc_fence_after();
                 const int64_t at = (int64_t)(u.c0 + tok) * p.num_q_heads + hq;
-                uint32_t o[64];
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    uint32_t x[2][32];
-                    tmem_ld32_async(lane_tm + 256 * t + 128 + 64 * c, x[0]);
-                    tmem_ld32_async(lane_tm + 256 * t + 128 + 64 * c + 32, x[1]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int e = 0; e < 32; e++)
-                        o[32 * c + e] = E::pack(__uint_as_float(x[e >> 4][2 * (e & 15)]) * inv,
-                                                __uint_as_float(x[e >> 4][2 * (e & 15) + 1]) * inv);
-                }
-                // O may be written again before this one's stores, which take far longer than its loads
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.o_free[t]);
                 // The rows leave through shared memory, 4 of 128 bytes an instruction: 16 bytes a lane of 32
                 // rows straight from registers hold up every other warp's shared-memory access.
                 const int64_t at0 = (int64_t)(u.c0 + u.tok0) * p.num_q_heads + u.h * G;
@@ -478,11 +462,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 for (int half = 0; half < 2; half++) {
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 8; c++)
-                        *reinterpret_cast<uint4 *>(stage + lane * kOutPitch + 16 * c) =
-                            make_uint4(o[32 * half + 4 * c], o[32 * half + 4 * c + 1], o[32 * half + 4 * c + 2],
-                                       o[32 * half + 4 * c + 3]);
+                    for (int c = 0; c < 2; c++) {
+                        uint32_t x[32], o[16];
+                        tmem_ld32_async(lane_tm + 256 * t + 128 + 64 * half + 32 * c, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; e++)
+                            o[e] = E::pack(__uint_as_float(x[2 * e]) * inv, __uint_as_float(x[2 * e + 1]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            *reinterpret_cast<uint4 *>(stage + lane * kOutPitch + 64 * c + 16 * e) =
+                                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                    if (half == 1) tc_fence_before();
                     __syncwarp();
+                    if (half == 1 && lane == 0) mbar_arrive(&sm.o_free[t]);  // O may be written again
 #pragma unroll
                     for (int k = 0; k < 8; k++) {
                         const int to = __shfl_sync(kFull, rel, 4 * k + (lane >> 3));
@@ -571,7 +565,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 for (int i = 0; i < sp.total && ok; i++) {
                     // O += P(i) V(i), in the parts that the softmax hands over, then S(i + 1); the
-                    // tiles take turns, so that one's softmax runs while the other's MMAs do
+                    // tiles take turns (one without this step passes its own on), so that one's softmax runs
+                    // while the other's MMAs do
                     const bool live = i < nst, more = i + 1 < nst;
                     const uint32_t stage_v = ring.stage;
                     ring.next();
@@ -579,11 +574,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     // (the next K's wait ahead of the turn: nothing comes between this PV and the next S)
                     if (i + 1 < sp.total) ok = ok && wait_full(ring.stage);
                     if (live) ok = ok && mbar_wait_short(&sm.p_full[t][0], p_phase);
-                    const bool both = i < min(sp.steps[0], sp.steps[1]);
-                    if (both) {
-                        ok = ok && mbar_wait_short(&sm.turn[t], turn_phase);
-                        turn_phase ^= 1u;
-                    }
+                    ok = ok && mbar_wait_short(&sm.turn[t], turn_phase);
+                    turn_phase ^= 1u;
                     if (!ok) break;
                     if (live) {
                         const uint32_t c = v_lo + stage_v * kStep;
@@ -600,14 +592,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         if (!ok) break;
                         p_phase ^= 1u;
                         if (more)
-                            issue_s(ring.stage, both);
+                            issue_s(ring.stage, true);
                         else
                             umma_commit(&sm.o_full[t]);
                         umma_commit(&sm.kv_free[stage_v]);
                     } else {
                         mbar_arrive(&sm.kv_free[stage_v]);
                     }
-                    if (both && !more) mbar_arrive(&sm.turn[t ^ 1]);
+                    if (!more) mbar_arrive(&sm.turn[t ^ 1]);
                     if (i + 1 < sp.total) {
                         if (more)
                             umma_commit(&sm.kv_free[ring.stage]);
