@@ -25,18 +25,18 @@
 //             wait for: behind the softmax they were late by hundreds of cycles.)
 //   1         walks the unit list and issues the copies of K and V (TMA) into a
 //             ring of four 32 KB stages.
-//   3         issues the copies of the Q tiles.
+//   3         issues the copies of the Q tiles.  The last step(s) of a unit hold
+//             keys past some row's position: of their V this warp zeroes the rows
+//             past the sequence's end and takes out values that are not finite
+//             (0 * inf would reach rows that do not see them; the epilogue adds
+//             them to the rows that do).
 //   4-7, 8-11 softmax of tile 0, tile 1: one thread per query row.  A row of S
 //             (128 scores) is read into registers once; maximum, 2^(s - m), the
 //             row sum in binary32; P rounded to the operands' type (the tensor
 //             cores take nothing wider) goes over S in three parts.  The running
 //             maximum is lazy: O is rescaled only when a row's maximum grows by
 //             more than 2^8, so P stays in [0, 256].
-//   12-15     the last step(s) of a unit hold keys past some row's position:
-//             their V rows past the sequence's end are zeroed and values that
-//             are not finite taken out (0 * inf would reach rows that do not see
-//             them; the epilogue adds them to the rows that do).  Then the
-//             epilogue: O / l, while the tensor cores are on the next unit.
+//   12-15     the epilogue: O / l, while the tensor cores are on the next unit.
 // While one tile's rows are in the softmax, the tensor cores work on the other.
 //
 // Unit order: cache heads in groups whose keys and values fit half of L2 (each
@@ -98,6 +98,16 @@ struct Elem {
             return f16x2_rn(a, b);
         }
     }
+    // the larger magnitudes of two pairs, a NaN if there is one
+    __device__ static __forceinline__ uint32_t larger(uint32_t a, uint32_t b)
+    {
+        uint32_t d;
+        if constexpr (BF)
+            asm("{\n\t.reg .b32 x;\n\tabs.bf16x2 x, %2;\n\tmax.NaN.bf16x2 %0, %1, x;\n\t}" : "=r"(d) : "r"(a), "r"(b));
+        else
+            asm("{\n\t.reg .b32 x;\n\tabs.f16x2 x, %2;\n\tmax.NaN.f16x2 %0, %1, x;\n\t}" : "=r"(d) : "r"(a), "r"(b));
+        return d;
+    }
     // bit 15 / 31 set where the pair's low / high value is not finite
     __device__ static __forceinline__ uint32_t wild(uint32_t w) { return ((w & kExp) + kOne) & 0x80008000u; }
     __device__ static __forceinline__ float value(uint16_t x)
@@ -132,6 +142,7 @@ struct alignas(1024) PromptSmem {
     uint64_t mma_done;
     float2 ml[kUnitTiles][kTileRows];
     PromptUnit unit[2];
+    uint32_t wild[4];  // by unit: some value of a mixed step is not finite (warp 3 may be two units ahead)
     uint32_t tmem;
 };
 static_assert(sizeof(PromptSmem) <= 227 * 1024, "one CTA's shared memory");
@@ -185,19 +196,6 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// barrier 1 over the four epilogue warps, returning whether any thread passed `v`
-__device__ __forceinline__ bool epilogue_any(bool v)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v)
-        : "memory");
-    return r != 0;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -223,7 +221,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mbar_init(&sm.kv_full[s], 1);
             mbar_init(&sm.kv_free[s], 2);  // both MMA threads
             mbar_init(&sm.kv_raw[s], 1);
-            mbar_init(&sm.kv_clean[s], 4);
+            mbar_init(&sm.kv_clean[s], 1);
         }
         for (int t = 0; t < kUnitTiles; t++) {
             mbar_init(&sm.q_full[t], 1);
@@ -237,7 +235,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         }
         for (int s = 0; s < 2; s++) {
             mbar_init(&sm.unit_full[s], 1);
-            mbar_init(&sm.unit_free[s], 15);  // 8 softmax warps, 4 epilogue warps, 2 MMA threads, the Q thread
+            mbar_init(&sm.unit_free[s], 15);  // 8 softmax warps, 4 epilogue warps, 2 MMA threads, warp 3
         }
         mbar_init(&sm.mma_done, 2);
         mbar_init_fence();
@@ -382,64 +380,18 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             done++;
         }
     } else if (warp >= 12) {
-        // ---- V of the mixed steps, then the epilogue ----
+        // ---- the epilogue ----
         regs_dec<kRegsEpilogue>();
-        const int w = tid & 127, row = w;
+        const int row = tid & 127;
         const uint32_t lane_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        Ring ring;
-        uint32_t raw_phase = 0;  // bit s: parity of stage s's next mixed V
         uint32_t done[kUnitTiles] = {0, 0};
-        for (int r = 0;; r++) {
+        for (int r = 0; ok; r++) {
             PromptUnit u;
-            if (ok) ok = __all_sync(kFull, fetch(r, u));
+            ok = __all_sync(kFull, fetch(r, u));
             __syncwarp();
             if (lane == 0 && ok) mbar_arrive(&sm.unit_free[r & 1]);
-            // a warp whose wait ran out meets the others here, so that all four leave together
-            if (epilogue_any(!ok)) {
-                ok = false;
-                break;
-            }
-            if (u.n < 0) break;
+            if (!ok || u.n < 0) break;
             const Span sp(u, p);
-            bool wild = false;
-            for (int i = 0; i < sp.total && ok; i++) {
-                ring.next();
-                if (i >= sp.mixed) {
-                    ok = __all_sync(kFull, mbar_wait_short(&sm.kv_raw[ring.stage], raw_phase >> ring.stage & 1u));
-                    if (!ok) break;
-                    raw_phase ^= 1u << ring.stage;
-                    uint8_t *v = sm.kv[ring.stage];
-                    const int left = u.n - i * kKeys;  // keys of the step inside the sequence
-                    uint4 *piece = reinterpret_cast<uint4 *>(v);
-                    auto key_of = [](int e) { return (e & 1023) >> 3; };  // 8 pieces a key, two halves of the elements
-                    uint32_t odd = 0;
-#pragma unroll 4
-                    for (int e = w; e < kTileBytes / 16; e += 128) {
-                        const uint4 x = piece[e];
-                        if (key_of(e) >= left)
-                            piece[e] = make_uint4(0u, 0u, 0u, 0u);
-                        else
-                            odd |= E::wild(x.x) | E::wild(x.y) | E::wild(x.z) | E::wild(x.w);
-                    }
-                    if (odd) {
-                        wild = true;
-                        uint32_t *word = reinterpret_cast<uint32_t *>(v);
-#pragma unroll 1
-                        for (int e = w; e < kTileBytes / 16; e += 128)
-#pragma unroll 1
-                            for (int c = 0; c < 4; c++) {
-                                const uint32_t m = E::wild(word[4 * e + c]);
-                                if (m & 0x8000u) word[4 * e + c] &= 0xFFFF0000u;
-                                if (m & 0x80000000u) word[4 * e + c] &= 0x0000FFFFu;
-                            }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.kv_clean[ring.stage]);
-                }
-                ring.next();  // V
-            }
-            wild = epilogue_any(wild);
 #pragma unroll 1
             for (int t = 0; t < sp.active && ok; t++) {
                 ok = __all_sync(kFull, mbar_wait_short(&sm.ml_full[t], done[t] & 1u));
@@ -452,6 +404,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 if (!ok) break;
                 done[t]++;
                 tc_fence_after();
+                const bool wild = sm.wild[r & 3] != 0;
                 const int64_t at = (int64_t)(u.c0 + tok) * p.num_q_heads + hq;
                 // The rows leave through shared memory, 4 of 128 bytes an instruction: 16 bytes a lane of 32
                 // rows straight from registers hold up every other warp's shared-memory access.
@@ -733,29 +686,81 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     if (!mbar_wait_short(raw ? &sm.kv_raw[s] : &sm.kv_full[s], next ^ 1u)) ok = false;
                 }
             }
-        } else if (warp == 3 && lane == 0) {
-            // ---- Q tiles: apart from K and V, whose copies would wait behind a tile in use ----
+        } else if (warp == 3) {
+            // ---- Q tiles (apart from K and V, whose copies would wait behind a tile in use), then
+            // the V of the mixed steps ----
             uint32_t uses[kUnitTiles] = {0, 0};
+            Ring ring;
+            uint32_t raw_phase = 0;  // bit s: parity of stage s's next mixed V
             for (int r = 0; ok; r++) {
                 PromptUnit u;
-                if (!fetch(r, u)) break;
-                mbar_arrive(&sm.unit_free[r & 1]);
-                if (u.n < 0) break;
+                ok = __all_sync(kFull, fetch(r, u));
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(&sm.unit_free[r & 1]);
+                if (!ok || u.n < 0) break;
                 const Span sp(u, p);
+                if (lane == 0) {
+                    sm.wild[r & 3] = 0u;
 #pragma unroll
-                for (int t = 0; t < kUnitTiles; t++) {
-                    if (t >= sp.active || !ok) continue;
-                    if (uses[t] > 0) ok = mbar_wait_short(&sm.q_free[t], (uses[t] - 1) & 1u);
-                    if (!ok) continue;
-                    mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * th * tt);
-                    const int tok = u.c0 + u.tok0 + t * p.tile1_token, hq = u.h * G + t * p.tile1_head;
-                    tma_load_3d(sm.q[t], &map_q, 0, hq, tok, &sm.q_full[t]);
-                    tma_load_3d(sm.q[t] + kTileBytes / 2, &map_q, 64, hq, tok, &sm.q_full[t]);
-                    uses[t]++;
+                    for (int t = 0; t < kUnitTiles; t++) {
+                        if (t >= sp.active || !ok) continue;
+                        if (uses[t] > 0) ok = mbar_wait_short(&sm.q_free[t], (uses[t] - 1) & 1u);
+                        if (!ok) continue;
+                        mbar_arrive_expect_tx(&sm.q_full[t], 2u * 128u * th * tt);
+                        const int tok = u.c0 + u.tok0 + t * p.tile1_token, hq = u.h * G + t * p.tile1_head;
+                        tma_load_3d(sm.q[t], &map_q, 0, hq, tok, &sm.q_full[t]);
+                        tma_load_3d(sm.q[t] + kTileBytes / 2, &map_q, 64, hq, tok, &sm.q_full[t]);
+                        uses[t]++;
+                    }
+                }
+                ok = __all_sync(kFull, ok);
+#pragma unroll 1
+                for (int i = 0; i < sp.total && ok; i++) {
+                    ring.next();
+                    if (i >= sp.mixed) {
+                        ok = __all_sync(kFull, mbar_wait_short(&sm.kv_raw[ring.stage], raw_phase >> ring.stage & 1u));
+                        if (!ok) break;
+                        raw_phase ^= 1u << ring.stage;
+                        const int left = u.n - i * kKeys;  // keys of the step inside the sequence
+                        uint4 *piece = reinterpret_cast<uint4 *>(sm.kv[ring.stage]);
+                        auto key_of = [](int e) { return (e & 1023) >> 3; };  // 8 pieces a key, two halves of the elements
+                        if (left < kKeys) {
+#pragma unroll 1
+                            for (int e = lane; e < kTileBytes / 16; e += 32)
+                                if (key_of(e) >= left) piece[e] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        uint32_t top[2] = {0u, 0u};
+#pragma unroll 8
+                        for (int e = lane; e < kTileBytes / 16; e += 32) {
+                            const uint4 x = piece[e];
+                            top[0] = E::larger(E::larger(top[0], x.x), x.y);
+                            top[1] = E::larger(E::larger(top[1], x.z), x.w);
+                        }
+                        const uint32_t odd = E::wild(top[0]) | E::wild(top[1]);
+                        if (odd) {
+                            uint32_t *word = reinterpret_cast<uint32_t *>(piece);
+#pragma unroll 1
+                            for (int e = lane; e < kTileBytes / 16; e += 32)
+#pragma unroll 1
+                                for (int c = 0; c < 4; c++) {
+                                    const uint32_t m = E::wild(word[4 * e + c]);
+                                    if (m & 0x8000u) word[4 * e + c] &= 0xFFFF0000u;
+                                    if (m & 0x80000000u) word[4 * e + c] &= 0x0000FFFFu;
+                                }
+                        }
+                        fence_proxy_async_smem();
+                        const bool any = __any_sync(kFull, odd != 0);
+                        if (lane == 0) {
+                            if (any) sm.wild[r & 3] = 1u;
+                            mbar_arrive(&sm.kv_clean[ring.stage]);
+                        }
+                    }
+                    ring.next();
                 }
             }
-            for (int t = 0; t < kUnitTiles; t++)  // no copy in flight when the CTA ends
-                if (uses[t] > 0 && !mbar_wait_short(&sm.q_full[t], (uses[t] - 1) & 1u)) ok = false;
+            if (lane == 0)
+                for (int t = 0; t < kUnitTiles; t++)  // no copy in flight when the CTA ends
+                    if (uses[t] > 0 && !mbar_wait_short(&sm.q_full[t], (uses[t] - 1) & 1u)) ok = false;
         }
     }
     __syncwarp();
