@@ -4,6 +4,9 @@ refuses host tensors, and the plain 64-bit forms that the GPU tests compare
 with are pinned by closed forms."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -100,6 +103,17 @@ def test_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         c = torch.zeros(1, 2, 64, 64, dtype=torch.uint8)
         kvq.PagedKVCache.over(0, c, c, torch.zeros(1, 2), torch.zeros(1, 2))
+
+
+def test_nvtx_ranges_wrap_the_entry_points():
+    code = ("from quantized_kv_cache_09_gb300 import kvq\n"
+            "print(*(hasattr(getattr(kvq, n), '__wrapped__') for n in "
+            "('kvq_prompt_attention', 'kvq_page_weights', 'kvq_evict_pages')))\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for value, want in (("1", "True True True"), ("0", "False False False")):
+        run = subprocess.run([sys.executable, "-c", code], cwd=root, env=dict(os.environ, KVQ_NVTX=value),
+                             capture_output=True, text=True, check=True)
+        assert run.stdout.strip() == want
 
 
 def test_plain_prompt_closed_forms():
