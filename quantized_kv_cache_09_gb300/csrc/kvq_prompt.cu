@@ -20,9 +20,7 @@
 //   0, 2      one thread each issues the MMAs of a tile: S = Q K^T, O += P V,
 //             M = N = 128.  (An MMA holds its issuer until the tensor pipe takes it,
 //             and a wait between MMAs costs ~100 cycles: with one thread for both
-//             tiles the pipe was busy 49% of the time.  The scheduler favours the
-//             lower warps, and these few instructions are the ones that others
-//             wait for: behind the softmax they were late by hundreds of cycles.)
+//             tiles the pipe was busy 49% of the time.)
 //   1         walks the unit list and issues the copies of K and V (TMA) into a
 //             ring of four 32 KB stages.
 //   3         issues the copies of the Q tiles.  The last step(s) of a unit hold
@@ -37,11 +35,21 @@
 //             maximum is lazy: O is rescaled only when a row's maximum grows by
 //             more than 2^8, so P stays in [0, 256].
 //   12-15     the epilogue: O / l, while the tensor cores are on the next unit.
-// While one tile's rows are in the softmax, the tensor cores work on the other.
+// While one tile's rows are in the softmax, the tensor cores work on the other:
+// the MMA threads take turns, [O += P V, next S] of one tile after the other.
+// Without the order both tiles' softmaxes fall together and the pipe idles (16384
+// tokens x 64 heads: 3.8 ms against 2.9).
 //
-// Unit order: cache heads in groups whose keys and values fit half of L2 (each
-// level reads them again: 8 x 2048 x 32 heads without groups read 1.2 GB from
-// HBM for 268 MB of keys and values); of a group by the number of the unit in
+// Measured (GB300): 16384 tokens x 64 / 8 heads 2.9 ms alone, 3.06 ms back to
+// back at the power cap (1.44 - 1.52 PFLOP/s, 0.75 - 0.79 of the measured bf16
+// rate); 8 x 2048 tokens x 32 heads 268 us (1.03 PFLOP/s), where a unit has 8.5
+// steps: its first and last steps, O's way out and the turn between units cost
+// about as much as three of them.  A steady step of both tiles takes ~2900 cycles
+// for 2048 of MMAs: half as many loads or no exponentials at all gain 4% each.
+//
+// Unit order: cache heads in groups whose keys and values fit half of L2, since
+// each level reads them again (8 x 2048 x 32 heads, 268 MB of them: 265 us, 282
+// without groups, 284 with groups of 32 or 96 MB); of a group by the number of the unit in
 // its sequence, the highest (most keys) first, over sequences and heads, dealt
 // to the CTAs forwards and backwards in turn -- longest first without a counter
 // to fetch from.
@@ -606,6 +614,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             int x = top, h0 = top < 0 ? H : 0, hn = hg;
             int64_t base = 0;      // units before level x of the heads from h0 on
             int count = level(x);  // sequences on level x
+            int at = 0, passed = 0;  // of the level's: `passed` come before sequence `at`, a multiple of 32
             Ring ring;
             uint32_t used = 0;  // stages filled so far, up to kStages
             // bit s: parity of stage s's next kv_full, kv_raw; whether its last fill was a mixed V
@@ -620,27 +629,26 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                         x = top;
                     }
                     count = level(x);
+                    at = passed = 0;
                 }
                 PromptUnit u = {0, -1, 0, 0};
                 if (h0 < H) {
                     const uint32_t rank = (uint32_t)(id - base);  // (at most 65535 sequences x 65535 heads)
-                    int k = (int)(rank / (uint32_t)hn);           // the k-th sequence of the level
+                    const int k = (int)(rank / (uint32_t)hn);     // the k-th sequence of the level
                     u.h = h0 + (int)(rank % (uint32_t)hn);
+                    // (its units come in order: the search goes on where the last one ended)
+                    uint32_t m = longer(at, x);
 #pragma unroll 1
-                    for (int b0 = 0;; b0 += 32) {
-                        uint32_t m = longer(b0, x);
-                        const int c = __popc(m);
-                        if (k >= c) {
-                            k -= c;
-                            continue;
-                        }
-#pragma unroll 1
-                        for (; k > 0; k--) m &= m - 1u;
-                        const int b = b0 + __ffs(m) - 1;
-                        u.c0 = p.cu[b];
-                        u.n = p.cu[b + 1] - u.c0;
-                        break;
+                    while (k >= passed + __popc(m) && at + 32 < p.num_seqs) {
+                        passed += __popc(m);
+                        at += 32;
+                        m = longer(at, x);
                     }
+#pragma unroll 1
+                    for (int skip = k - passed; skip > 0; skip--) m &= m - 1u;
+                    const int b = min(at + max(__ffs(m) - 1, 0), p.num_seqs - 1);
+                    u.c0 = p.cu[b];
+                    u.n = p.cu[b + 1] - u.c0;
                     u.tok0 = x * ut;
                 }
                 ok = __all_sync(kFull, r < 2 || mbar_wait_short(&sm.unit_free[r & 1], (uint32_t)((r >> 1) - 1) & 1u));

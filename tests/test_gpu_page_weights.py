@@ -129,6 +129,47 @@ def test_bad_tables_and_lengths(cuda_ok):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_more_rows_than_the_bound_are_flagged(cuda_ok):
+    b = Batch(kvq.KVQ_INT4_B64, [300, 200], [3, 2], 2, 2, seed=13)
+    want = b.check()
+    b.max_rows = 2
+    got = b.run()
+    torch.cuda.synchronize()
+    assert kvq.kvq_get_device_status(b.cache)[1] == kvq.KVQ_FLAG_BAD_LENGTH
+    assert got[0].isnan().all() and torch.equal(got[1], want[1])
+
+
+def test_no_rows_at_all(cuda_ok):
+    """A call without a single query keeps every weight."""
+    b = Batch(kvq.KVQ_INT4_B64, [300, 200], [1, 1], 2, 2, seed=14)
+    out = torch.full_like(b.before, math.nan)
+    kvq.kvq_page_weights(b.cache, b.q[:0], _i32([0, 0, 0]), 4, b.table, b.lens, SM, 0.5, b.before, out, b.ws)
+    kvq.kvq_page_weights(b.cache, b.q[:0], _i32([0, 0, 0]), 0, b.table, b.lens, SM, 0.5, b.before, out, b.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, b.before) and kvq.kvq_get_device_status(b.cache) == (0, 0)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_large_groups(cuda_ok, rows):
+    """A single cache head under 200 query heads."""
+    Batch(kvq.KVQ_FP8_E4M3, [130, 700], [rows, 1], 1, 200, seed=15).check()
+
+
+def test_two_calls_at_once(cuda_ok):
+    """Two streams, each with its own workspace, over one cache."""
+    b = Batch(kvq.KVQ_INT8_PAGE, [3000, 900, 64], [20, 3, 1], 4, 4, seed=16)
+    want = b.check()
+    other = kvq.page_weights_workspace(b.q.shape[0], b.q.shape[1], b.table.shape[1])
+    outs = [torch.empty_like(want) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, o, w in zip(streams, outs, (b.ws, other)):
+            kvq.kvq_page_weights(b.cache, b.q, b.cu, b.max_rows, b.table, b.lens, SM, 1.0, b.before, o, w, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
 def test_nan_in_keys_after_the_positions(cuda_ok):
     """Rows of an open page past the sequence's end are read but carry no weight, whatever they hold."""
     b = Batch(kvq.KVQ_FP8_E4M3, [100], [1], 1, 1, seed=10)

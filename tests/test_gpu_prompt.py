@@ -132,6 +132,12 @@ def test_many_sequences(cuda_ok):
     _check(*_inputs([1 + (i * 53) % 140 for i in range(90)], 4, 1, torch.float16, seed=7))
 
 
+def test_thousands_of_short_prompts(cuda_ok):
+    """A batch whose every prompt is a few tokens, some empty, in several head groups of units."""
+    lens = [(i * 7) % 12 for i in range(3000)]
+    _check(*_inputs(lens, 2, 2, torch.float16, seed=14))
+
+
 def test_without_lse_and_repeatable(cuda_ok):
     q, k, v, cu = _inputs([600, 128], 8, 1, torch.float16, seed=8)
     want, _, _ = _run(q, k, v, cu)
