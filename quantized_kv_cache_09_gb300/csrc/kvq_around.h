@@ -6,9 +6,26 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kvq.h"
 
 namespace kvq {
+
+// let `kernel` take `bytes` of dynamic shared memory on the current device; `done`, one per kernel,
+// remembers the devices (64 of them) that know it
+template <typename K>
+cudaError_t allow_smem(K *kernel, size_t bytes, std::atomic<uint64_t> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // query heads per cache head that share a 128-row tile of prompt attention
 constexpr int kMaxPromptGroup = 128;

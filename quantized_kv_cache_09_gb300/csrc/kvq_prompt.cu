@@ -823,9 +823,9 @@ cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t
         !make_map(&mk, BF, k, p.total, p.num_heads, k_stride, 1, kKeys) ||
         !make_map(&mv, BF, p.v, p.total, p.num_heads, p.v_stride, 1, kKeys))
         return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done[2] = {0, 0};
     auto kernel = p.score_scale < 0.0f ? prompt_attn_kernel<BF, true> : prompt_attn_kernel<BF, false>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(PromptSmem));
+    const cudaError_t e = allow_smem(kernel, sizeof(PromptSmem), done[p.score_scale < 0.0f]);
     if (e != cudaSuccess) return e;
     // at most one CTA per SM, and no more than there can be units
     const int64_t ut = p.unit_tokens;

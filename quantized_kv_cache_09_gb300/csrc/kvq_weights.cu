@@ -550,8 +550,8 @@ __global__ void __launch_bounds__(kSumThreads) page_join_kernel(PageWeightsParam
 template <int FMT, int NT>
 static cudaError_t launch_page_lse(const PageWeightsParams &p, int num_sms, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(page_lse_kernel<FMT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(PwSmem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(page_lse_kernel<FMT, NT>, sizeof(PwSmem), done);
     if (e != cudaSuccess) return e;
     return launch_pdl(page_lse_kernel<FMT, NT>, dim3((unsigned)num_sms), dim3(kPwWarps * 32), sizeof(PwSmem), s, p);
 }

@@ -463,8 +463,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
 template <int FMT>
 static cudaError_t launch_page_window_fmt(const PageWeightsParams &p, int num_sms, cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(page_window_kernel<FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(WinSmem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(page_window_kernel<FMT>, sizeof(WinSmem), done);
     if (e != cudaSuccess) return e;
     return launch_pdl(page_window_kernel<FMT>, dim3((unsigned)num_sms), dim3(kWinThreads), sizeof(WinSmem), s, p);
 }

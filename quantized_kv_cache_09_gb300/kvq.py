@@ -9,7 +9,6 @@ entry point that launches work is wrapped in an NVTX range named after its C
 function, for profilers that filter by range (ncu --nvtx --nvtx-include ...);
 unset, the wrappers are the plain functions.
 """
-import contextlib
 import ctypes
 import functools
 import os
@@ -162,24 +161,29 @@ def lib():
     return _lib
 
 
-_current_device = torch.cuda.current_device
-
-
-def _on(index):
-    """A context with device `index` current: none where it already is (entering one costs more than a launch's
-    other host work)."""
-    return _NOTHING if index == _current_device() else torch.cuda.device(index)
-
-
-_NOTHING = contextlib.nullcontext()
-
-
-def _dense(index, dtype, **tensors):
-    """Refuse what is no contiguous tensor of dtype on CUDA device `index`."""
-    for name, t in tensors.items():
+def _dense(index, dtype, names, *tensors):
+    """Refuse what is no contiguous tensor of dtype on CUDA device `index` (names: one word each)."""
+    for t in tensors:
         if t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index or index < 0:
+            name = names.split()[[x is t for x in tensors].index(True)]
             _cuda(t, dtype, name)
             raise ValueError(f"{name} is on another device")
+
+
+def _call(fn, index, stream, *args):
+    """fn(*args, stream) with device `index` current (entered only where another is: that costs more than a
+    launch's other host work); stream None: the device's current one."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        raw = _stream(stream)
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != 0:
+        raise KvqError(rc, fn.__name__)
 
 
 def _ptr(t):
@@ -189,7 +193,8 @@ def _ptr(t):
 def _stream(stream, device=None):
     if stream is None:
         index = None if device is None else torch.device(device).index
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(_current_device() if index is None else index))
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None
+                                                                  else index))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -382,24 +387,21 @@ def kvq_prompt_attention(q, k, v, cu_seqlens, max_tokens_per_seq, softmax_scale,
         raise ValueError("q must be a CUDA float16 or bfloat16 tensor")
     dev = q.get_device()
     qs, ks, vs = _rows(q, dtype, dev, "q"), _rows(k, dtype, dev, "k"), _rows(v, dtype, dev, "v")
-    _dense(dev, dtype, out=out)
-    _dense(dev, torch.int32, cu_seqlens=cu_seqlens)
+    _dense(dev, dtype, "out", out)
+    _dense(dev, torch.int32, "cu_seqlens", cu_seqlens)
     if lse is not None:
-        _dense(dev, torch.float32, lse=lse)
+        _dense(dev, torch.float32, "lse", lse)
     if status is not None:
-        _dense(dev, torch.int32, status=status)
+        _dense(dev, torch.int32, "status", status)
     T, Hq, _ = q.shape
     n = cu_seqlens.numel() - 1
     if (out.shape != q.shape or k.shape != v.shape or k.shape[0] != T or cu_seqlens.dim() != 1 or n < 0 or
             (lse is not None and lse.shape != (T, Hq)) or (status is not None and status.numel() < 1)):
         raise ValueError("q/k/v/out/lse/cu_seqlens shapes disagree")
-    with _on(dev):
-        _check(lib().kvq_prompt_attention(KVQ_BF16 if dtype is torch.bfloat16 else KVQ_FP16, q.data_ptr(), qs,
-                                          k.data_ptr(), ks, v.data_ptr(), vs, Hq, k.shape[1], HEAD_DIM,
-                                          cu_seqlens.data_ptr(), T, int(max_tokens_per_seq), n, float(softmax_scale),
-                                          out.data_ptr(), None if lse is None else lse.data_ptr(),
-                                          None if status is None else status.data_ptr(), _stream(stream, q.device)),
-               "kvq_prompt_attention")
+    _call(lib().kvq_prompt_attention, dev, stream, KVQ_BF16 if dtype is torch.bfloat16 else KVQ_FP16, q.data_ptr(), qs,
+          k.data_ptr(), ks, v.data_ptr(), vs, Hq, k.shape[1], HEAD_DIM, cu_seqlens.data_ptr(), T,
+          int(max_tokens_per_seq), n, float(softmax_scale), out.data_ptr(), None if lse is None else lse.data_ptr(),
+          None if status is None else status.data_ptr())
 
 
 def kvq_page_weights_workspace_bytes(total_q, num_q_heads, max_blocks_per_seq):
@@ -421,24 +423,19 @@ def kvq_page_weights(cache, q, cu_seqlens_q, max_q_per_seq, block_table, seq_len
     its last tokens; one row each in a decode step), summed over heads and
     queries.  weights_out may be weights_in."""
     dev = q.get_device()
-    _dense(dev, torch.float16, q=q)
-    _dense(dev, torch.int32, cu_seqlens_q=cu_seqlens_q, block_table=block_table, seq_lens=seq_lens)
-    _dense(dev, torch.float32, weights_out=weights_out)
-    if weights_in is not None:
-        _dense(dev, torch.float32, weights_in=weights_in)
-    _dense(dev, torch.uint8, workspace=workspace)
+    _dense(dev, torch.float16, "q", q)
+    _dense(dev, torch.int32, "cu_seqlens_q block_table seq_lens", cu_seqlens_q, block_table, seq_lens)
+    _dense(dev, torch.float32, "weights_out weights_in", weights_out, weights_out if weights_in is None else weights_in)
+    _dense(dev, torch.uint8, "workspace", workspace)
     B = seq_lens.numel()
-    if (q.dim() != 3 or q.shape[2] != HEAD_DIM or cu_seqlens_q.numel() != B + 1 or block_table.dim() != 2 or
-            block_table.shape[0] != B or weights_out.shape != block_table.shape or
-            (weights_in is not None and weights_in.shape != block_table.shape)):
+    shape, rows = block_table.shape, q.shape
+    if (len(rows) != 3 or rows[2] != HEAD_DIM or cu_seqlens_q.numel() != B + 1 or len(shape) != 2 or shape[0] != B or
+            weights_out.shape != shape or (weights_in is not None and weights_in.shape != shape)):
         raise ValueError("q/cu_seqlens_q/seq_lens/block_table/weights shapes disagree")
-    with _on(dev):
-        _check(lib().kvq_page_weights(ctypes.byref(cache.struct), q.data_ptr(), q.shape[1], cu_seqlens_q.data_ptr(),
-                                      q.shape[0], int(max_q_per_seq), block_table.data_ptr(), block_table.shape[1],
-                                      seq_lens.data_ptr(), B, float(softmax_scale), float(decay),
-                                      None if weights_in is None else weights_in.data_ptr(), weights_out.data_ptr(),
-                                      workspace.data_ptr(), workspace.numel(), _stream(stream, q.device)),
-               "kvq_page_weights")
+    _call(lib().kvq_page_weights, dev, stream, ctypes.byref(cache.struct), q.data_ptr(), rows[1],
+          cu_seqlens_q.data_ptr(), rows[0], int(max_q_per_seq), block_table.data_ptr(), shape[1], seq_lens.data_ptr(), B,
+          float(softmax_scale), float(decay), None if weights_in is None else weights_in.data_ptr(),
+          weights_out.data_ptr(), workspace.data_ptr(), workspace.numel())
 
 
 @_nvtx
@@ -450,25 +447,22 @@ def kvq_evict_pages(block_table, seq_lens, weights, keep_blocks, sink_blocks, re
     the entries past the length, then the num_evicted[b] evicted pages;
     seq_lens_out and weights_out follow.  An output may be its own input."""
     dev = block_table.get_device()
-    _dense(dev, torch.int32, block_table=block_table, seq_lens=seq_lens, keep_blocks=keep_blocks, table_out=table_out,
-           seq_lens_out=seq_lens_out, num_evicted=num_evicted)
-    _dense(dev, torch.float32, weights=weights, weights_out=weights_out)
+    _dense(dev, torch.int32, "block_table seq_lens keep_blocks table_out seq_lens_out num_evicted", block_table,
+           seq_lens, keep_blocks, table_out, seq_lens_out, num_evicted)
+    _dense(dev, torch.float32, "weights weights_out", weights, weights_out)
     if status is not None:
-        _dense(dev, torch.int32, status=status)
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [num_seqs][max_blocks_per_seq]")
+        _dense(dev, torch.int32, "status", status)
     shape = block_table.shape
+    if len(shape) != 2:
+        raise ValueError("block_table must be [num_seqs][max_blocks_per_seq]")
     B, mb = shape
     if (table_out.shape != shape or weights.shape != shape or weights_out.shape != shape or seq_lens.numel() != B or
             keep_blocks.numel() != B or seq_lens_out.numel() != B or num_evicted.numel() != B or
             (status is not None and status.numel() < 1)):
         raise ValueError("block_table/seq_lens/weights/keep_blocks shapes disagree")
-    with _on(dev):
-        _check(lib().kvq_evict_pages(block_table.data_ptr(), mb, seq_lens.data_ptr(), weights.data_ptr(), B,
-                                     keep_blocks.data_ptr(), int(sink_blocks), int(recent_blocks),
-                                     table_out.data_ptr(), seq_lens_out.data_ptr(), weights_out.data_ptr(),
-                                     num_evicted.data_ptr(), None if status is None else status.data_ptr(),
-                                     _stream(stream, block_table.device)), "kvq_evict_pages")
+    _call(lib().kvq_evict_pages, dev, stream, block_table.data_ptr(), mb, seq_lens.data_ptr(), weights.data_ptr(), B,
+          keep_blocks.data_ptr(), int(sink_blocks), int(recent_blocks), table_out.data_ptr(), seq_lens_out.data_ptr(),
+          weights_out.data_ptr(), num_evicted.data_ptr(), None if status is None else status.data_ptr())
 
 
 class StepGraph:
