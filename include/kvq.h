@@ -343,6 +343,8 @@ size_t kvq_prefill_workspace_bytes(int32_t num_q_heads, int32_t num_seqs, int32_
  *   max_tokens_per_seq  host bound on every length; 0 is a no-op
  *   status           one int32 for KVQ_FLAG_* bits (the cache's status word,
  *                    for instance), or NULL
+ * Launch: with programmatic dependent launch; everything is read after waiting
+ * for the previous kernel of the stream.
  * A sequence that breaks a bound is skipped and KVQ_FLAG_BAD_LENGTH set.
  * Errors: KVQ_ERR_INVALID_ARG, KVQ_ERR_UNSUPPORTED (head_dim != 128, unknown
  * dtype, g > 128, more than 65535 sequences or cache heads, total_tokens above 2^31 - 1),

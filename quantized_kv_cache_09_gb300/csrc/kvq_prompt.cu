@@ -204,6 +204,11 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -224,6 +229,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.group, tt = p.tile_tokens, th = p.tile_heads;
 
+    pdl_launch_dependents();
+    if (tid == 32) {
+        prefetch_map(&map_k);
+        prefetch_map(&map_v);
+        prefetch_map(&map_q);
+    }
     if (tid == 0) {
         for (int s = 0; s < kStages; s++) {
             mbar_init(&sm.kv_full[s], 1);
@@ -256,6 +267,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_wait();  // (nothing of global memory is read before it)
     const uint32_t tmem = sm.tmem;
     bool ok = true;
 
@@ -832,7 +844,7 @@ cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t
     const int64_t by_max = (int64_t)p.num_seqs * ((p.max_n + ut - 1) / ut), by_total = p.total / ut + p.num_seqs;
     const int64_t units = (by_max < by_total ? by_max : by_total) * p.num_heads;
     const int grid = units < num_sms ? (int)units : num_sms;
-    return launch_plain(kernel, dim3((unsigned)grid), dim3(kPromptThreads), sizeof(PromptSmem), s, p,
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kPromptThreads), sizeof(PromptSmem), s, p,
                         mq, mk, mv);
 }
 

@@ -443,9 +443,10 @@ __global__ void __launch_bounds__(kSumThreads, 2) page_sum_kernel(PageWeightsPar
     const int b = blockIdx.y, c = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
-    pdl_wait();
     PwSeq s;
-    if (!pw_seq(p, b, s)) return;
+    const bool good = pw_seq(p, b, s);
+    pdl_wait();  // (the lengths are read before it)
+    if (!good) return;
     const int np = (s.L + kPage - 1) / kPage, mb = p.max_blocks;
     const int64_t rows = (int64_t)s.n * p.num_q_heads, r0 = (int64_t)c * kPwSumRows;
     const float *in = p.weights_in ? p.weights_in + (int64_t)b * mb : nullptr;
@@ -504,6 +505,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) page_sum_kernel(PageWeightsPar
     for (int j0 = 0; j0 < (last ? mb : np); j0 += kTile) {
         const int j = j0 + jj;
         float a = 0.0f;
+        const float old = last && in && grp == 0 && j < np ? in[j] : 0.0f;
         if (j < np) {
 #pragma unroll
             for (int k = 0; k < kPwSumRows / kGroups; k++) {
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(kSumThreads, 2) page_sum_kernel(PageWeightsPar
             if (!last) {
                 if (j < np) part[j] = a;
             } else {
-                out[j] = j < np ? fmaf(p.decay, in ? in[j] : 0.0f, a) : 0.0f;
+                out[j] = j < np ? fmaf(p.decay, old, a) : 0.0f;
             }
         }
         __syncthreads();
@@ -528,9 +530,10 @@ __global__ void __launch_bounds__(kSumThreads, 2) page_sum_kernel(PageWeightsPar
 __global__ void __launch_bounds__(kSumThreads) page_join_kernel(PageWeightsParams p)
 {
     const int b = blockIdx.y, j = blockIdx.x * kSumThreads + threadIdx.x, mb = p.max_blocks;
-    pdl_wait();
     PwSeq s;
-    if (!pw_seq(p, b, s) || j >= mb) return;
+    const bool good = pw_seq(p, b, s);
+    pdl_wait();
+    if (!good || j >= mb) return;
     const int64_t rows = (int64_t)s.n * p.num_q_heads;
     if (rows <= kPwSumRows) return;
     const int np = (s.L + kPage - 1) / kPage;
