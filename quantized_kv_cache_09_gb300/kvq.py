@@ -427,6 +427,8 @@ def kvq_page_weights(cache, q, cu_seqlens_q, max_q_per_seq, block_table, seq_len
     _dense(dev, torch.int32, "cu_seqlens_q block_table seq_lens", cu_seqlens_q, block_table, seq_lens)
     _dense(dev, torch.float32, "weights_out weights_in", weights_out, weights_out if weights_in is None else weights_in)
     _dense(dev, torch.uint8, "workspace", workspace)
+    if cache.k_codes.get_device() != dev:
+        raise ValueError("the cache is on another device")
     B = seq_lens.numel()
     shape, rows = block_table.shape, q.shape
     if (len(rows) != 3 or rows[2] != HEAD_DIM or cu_seqlens_q.numel() != B + 1 or len(shape) != 2 or shape[0] != B or

@@ -1,6 +1,7 @@
 """kvq_page_weights against the plain 64-bit form, within the bound counted
 there from the operands' magnitudes."""
 import math
+import types
 
 import pytest
 import torch
@@ -187,6 +188,13 @@ def test_refusals(cuda_ok):
     with pytest.raises(ValueError, match="shapes"):
         kvq.kvq_page_weights(b.cache, b.q, b.cu, 1, b.table, b.lens, SM, 1.0, b.before[:, :1].contiguous(),
                              torch.empty_like(b.before), b.ws)
+
+
+def test_a_cache_on_another_device_is_refused(cuda_ok):
+    b = Batch(kvq.KVQ_INT8_PAGE, [100], [1], 1, 1, seed=11)
+    other = types.SimpleNamespace(struct=b.cache.struct, k_codes=types.SimpleNamespace(get_device=lambda: 1))
+    with pytest.raises(ValueError, match="another device"):
+        kvq.kvq_page_weights(other, b.q, b.cu, 1, b.table, b.lens, SM, 1.0, None, torch.empty_like(b.before), b.ws)
 
 
 def test_other_stream_and_graph(cuda_ok):
