@@ -59,7 +59,7 @@ struct PageWeightsParams {
     int64_t total_q;
     float score_scale;  // softmax_scale * log2(e)
     float decay;
-    float *lse;   // [total_q * num_q_heads][max_blocks]: log2-sum of a page's 2^score per query row
+    float *lse;   // total_q * num_q_heads * max_blocks log2-sums of a page's 2^score per query row
     float *part;  // [total_q * ceil(num_q_heads / 64)][max_blocks]: page masses of a chunk of rows
 };
 

@@ -211,9 +211,12 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     scales(32, ph[1], sk[1]);
 
     uint32_t qb[NT][8][2];       // the unit's query rows as the B operand: column g of tile nt is row row0 + 8 nt + g
-    float bias[NT][2];           // columns 2t, 2t + 1: minus the offset share of every raw score (int4)
-    float *dst[NT][2];           // their rows of the workspace
-    int pos[NT][2], pos0 = 0;    // their positions; the least position of the chunk
+    int pos[NT][2], pos0 = 0;    // columns 2t, 2t + 1: their positions; the least position of the chunk
+    // of column 2t + g % 2, whose sums this lane ends up with:
+    float bias[NT];              // minus the offset share of every raw score (int4)
+    float *dst[NT];              // its place in the workspace; the next page's is row_step on
+    uint32_t writes = 0;         // bit nt: a lane that writes one
+    int64_t row_step = 0;
     const float sign = p.score_scale < 0.0f ? -1.0f : 1.0f;
     const float sabs = fmaxf(fabsf(p.score_scale), kPwMinScale);
     bool ok = true;
@@ -243,6 +246,8 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
             const Place x = place(first + i);
             const int rows = x.s.n * G;
             pos0 = x.s.L - x.s.n;
+            row_step = (int64_t)x.s.n * p.num_q_heads;
+            writes = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
                 const int rr = x.row0 + 8 * nt + g;
@@ -293,15 +298,12 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
                         qb[nt][2 * m + 1][1] = v[m].w;
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    bias[nt][e] = -__shfl_sync(kFull, off, (2 * t + e) * 4);
-                    const int rc = x.row0 + 8 * nt + 2 * t + e;
-                    dst[nt][e] = rc < rows ? p.lse + ((int64_t)(x.s.c0 + rc / G) * p.num_q_heads + x.h * G + rc % G) *
-                                                         p.max_blocks
-                                           : nullptr;
-                    pos[nt][e] = pos0 + rc / G;
-                }
+                const int rc = x.row0 + 8 * nt + 2 * t;
+                bias[nt] = -__shfl_sync(kFull, off, (2 * t + (g & 1)) * 4);
+                dst[nt] = pw_sums(p, x.s) + j * row_step + (int64_t)x.h * rows + rc + (g & 1);
+                writes |= (uint32_t)(g < 2 && rc + (g & 1) < rows) << nt;
+                pos[nt][0] = pos0 + rc / G;
+                pos[nt][1] = pos0 + (rc + 1) / G;
             }
         }
 
@@ -414,9 +416,9 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
             l += __shfl_xor_sync(kFull, odd ? la : lb, 4);
             l += __shfl_xor_sync(kFull, l, 8);
             l += __shfl_xor_sync(kFull, l, 16);
-            float *d = odd ? dst[nt][1] : dst[nt][0];
-            const float mm = odd ? m[1] : m[0], bb = odd ? bias[nt][1] : bias[nt][0];
-            if (g < 2 && d) d[j] = fmaf(f, mm, FMT == KVQ_INT4_B64 ? bb * fac : 0.0f) + __log2f(l);
+            if (writes >> nt & 1u)
+                *dst[nt] = fmaf(f, odd ? m[1] : m[0], FMT == KVQ_INT4_B64 ? bias[nt] * fac : 0.0f) + __log2f(l);
+            dst[nt] += row_step;
         }
     }
     if (bad_page) set_flag(p.status, KVQ_FLAG_BAD_PAGE);
@@ -432,14 +434,16 @@ __global__ void __launch_bounds__(kPwWarps * 32, 1) page_lse_kernel(PageWeightsP
     }
 }
 
-// Rows [64 c, 64 c + 64) of sequence b (query rows, tokens x heads): the rows' log2-sums over
-// the pages (one pass: maximum and sum together), then each page's mass over these rows, to the
-// output (one chunk) or to `part`.
+// Rows [64 c, 64 c + 64) of sequence b: the rows' log2-sums over the pages, then each page's mass
+// over these rows, to the output (one chunk) or to `part`.  A lane has two rows, a warp every 16th
+// page; the pages go in blocks of 256, the first one last, so that it is still in registers for
+// the masses (up to 16K tokens are read once).
 __global__ void __launch_bounds__(kSumThreads, 2) page_sum_kernel(PageWeightsParams p)
 {
-    constexpr int kGroups = 4, kTile = kSumThreads / kGroups;  // a tile of pages x groups of rows
+    constexpr int kWarps = kSumThreads / 32, kPages = 16, kBlock = kWarps * kPages;
+    __shared__ float2 row_part[kWarps][kPwSumRows];  // maximum and sum of a warp's pages
     __shared__ float total[kPwSumRows];
-    __shared__ float sums[kGroups][kTile];
+    __shared__ float mass[kBlock];
     const int b = blockIdx.y, c = blockIdx.x;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     pdl_launch_dependents();
@@ -458,70 +462,79 @@ __global__ void __launch_bounds__(kSumThreads, 2) page_sum_kernel(PageWeightsPar
     }
     if (r0 >= rows) return;
     const int nr = (int)min((int64_t)kPwSumRows, rows - r0);
-    const float *lse = p.lse + ((int64_t)s.c0 * p.num_q_heads + r0) * mb;
-    constexpr int kRowsWarp = kPwSumRows / (kSumThreads / 32);  // a warp's rows, all in flight at once
-    {
-        float m[kRowsWarp], l[kRowsWarp];
+    const bool have[2] = {lane < nr, lane + 32 < nr};
+    const float *sums = pw_sums(p, s) + r0 + lane;
+    float v[kPages][2];
+    auto load = [&](int j0) {
 #pragma unroll
-        for (int i = 0; i < kRowsWarp; i++) {
-            m[i] = -INFINITY;
-            l[i] = 0.0f;
+        for (int i = 0; i < kPages; i++) {
+            const int j = j0 + i * kWarps + warp;
+            const float *at = sums + j * rows;
+#pragma unroll
+            for (int x = 0; x < 2; x++) v[i][x] = j < np && have[x] ? at[32 * x] : -INFINITY;
         }
-        for (int j0 = 0; j0 < np; j0 += 4 * 32) {
-            float v[kRowsWarp][4];
+    };
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int j0 = (np - 1) / kBlock * kBlock; j0 >= 0; j0 -= kBlock) {
+        load(j0);
 #pragma unroll
-            for (int i = 0; i < kRowsWarp; i++)
+        for (int x = 0; x < 2; x++) {
+            float top = m[x];
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const int r = warp * kRowsWarp + i, j = j0 + 32 * k + lane;
-                    v[i][k] = r < nr && j < np ? lse[(int64_t)r * mb + j] : -INFINITY;
-                }
+            for (int i = 0; i < kPages; i += 2) top = max3(top, v[i][x], v[i + 1][x]);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            l[x] *= ex2_approx(m[x] - ref);  // (m = -inf: the sum was 0)
 #pragma unroll
-            for (int i = 0; i < kRowsWarp; i++) {
-                const float top = fmaxf(max3(m[i], v[i][0], v[i][1]), fmaxf(v[i][2], v[i][3]));
-                const float ref = top == -INFINITY ? 0.0f : top;
-                l[i] *= ex2_approx(m[i] - ref);  // (m = -inf: the sum was 0)
-#pragma unroll
-                for (int k = 0; k < 4; k++) l[i] += ex2_approx(v[i][k] - ref);
-                m[i] = top;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRowsWarp; i++) {
-            float top = m[i];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-            float a = m[i] == -INFINITY ? l[i] : l[i] * ex2_approx(m[i] - top);  // (l = 0, or NaN)
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
-            if (lane == 0 && warp * kRowsWarp + i < nr) total[warp * kRowsWarp + i] = top + __log2f(a);
+            for (int i = 0; i < kPages; i++) l[x] += ex2_approx(v[i][x] - ref);
+            m[x] = top;
         }
     }
+    row_part[warp][lane] = make_float2(m[0], l[0]);
+    row_part[warp][lane + 32] = make_float2(m[1], l[1]);
     __syncthreads();
+    if (tid < kPwSumRows) {
+        float top = -INFINITY, a = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) top = fmaxf(top, row_part[w][tid].x);
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const float2 y = row_part[w][tid];
+            a += y.x == -INFINITY ? y.y : y.y * ex2_approx(y.x - top);  // (-inf: a sum of 0, or NaN)
+        }
+        total[tid] = tid < nr ? top + __log2f(a) : 0.0f;
+    }
+    __syncthreads();
+    const float t0 = total[lane], t1 = total[lane + 32];
     const bool last = rows <= kPwSumRows;  // the sequence's only chunk
     const int per_token = (p.num_q_heads + kPwSumRows - 1) / kPwSumRows;
     float *part = p.part + ((int64_t)s.c0 * per_token + c) * mb;
-    const int grp = tid / kTile, jj = tid % kTile;
-    for (int j0 = 0; j0 < (last ? mb : np); j0 += kTile) {
-        const int j = j0 + jj;
-        float a = 0.0f;
-        const float old = last && in && grp == 0 && j < np ? in[j] : 0.0f;
-        if (j < np) {
+    const int end = last ? mb : np;
+    for (int j0 = 0; j0 < end; j0 += kBlock) {
+        if (j0 > 0) load(j0);
+        // over the lanes: every exchange halves a lane's pages, the last one adds two lanes' sums of
+        // one page, (lane / 2) of the warp's 16
+        float a[kPages];
 #pragma unroll
-            for (int k = 0; k < kPwSumRows / kGroups; k++) {
-                const int r = grp * (kPwSumRows / kGroups) + k;
-                if (r < nr) a += ex2_approx(lse[(int64_t)r * mb + j] - total[r]);
+        for (int i = 0; i < kPages; i++) a[i] = ex2_approx(v[i][0] - t0) + ex2_approx(v[i][1] - t1);
+#pragma unroll
+        for (int o = 16, half = kPages / 2; half > 0; o >>= 1, half >>= 1) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < half; i++) {
+                const float mine = upper ? a[i + half] : a[i], other = upper ? a[i] : a[i + half];
+                a[i] = mine + __shfl_xor_sync(kFull, other, o);
             }
         }
-        sums[grp][jj] = a;
+        a[0] += __shfl_xor_sync(kFull, a[0], 1);
+        if ((lane & 1) == 0) mass[(lane >> 1) * kWarps + warp] = a[0];
         __syncthreads();
-        if (grp == 0 && j < mb) {
-            a = (sums[0][jj] + sums[1][jj]) + (sums[2][jj] + sums[3][jj]);
-            if (!last) {
-                if (j < np) part[j] = a;
-            } else {
-                out[j] = j < np ? fmaf(p.decay, old, a) : 0.0f;
-            }
+        const int j = j0 + tid;
+        if (tid < kBlock && j < end) {
+            const float w = j < np ? mass[tid] : 0.0f;
+            if (!last)
+                part[j] = w;
+            else
+                out[j] = j < np ? fmaf(p.decay, in ? in[j] : 0.0f, w) : 0.0f;
         }
         __syncthreads();
     }

@@ -38,6 +38,13 @@ __device__ __forceinline__ bool pw_seq(const PageWeightsParams &p, int b, PwSeq 
            (int64_t)s.c0 + s.n <= p.total_q;
 }
 
+// The workspace of a sequence's log2-sums: [page][query row], its rows by cache head, then by token
+// and head of the group, so that the rows of a tile lie side by side.
+__device__ __forceinline__ float *pw_sums(const PageWeightsParams &p, const PwSeq &s)
+{
+    return p.lse + (int64_t)s.c0 * p.num_q_heads * p.max_blocks;
+}
+
 // the least factor of a raw score: a key scale or softmax scale of 0 scores 1e-38 * raw instead of
 // 0 (no difference in binary32 once the maximum is subtracted), and a masked score stays -inf
 constexpr float kPwMinScale = 1.17549435e-38f;

@@ -39,7 +39,7 @@ constexpr int kWinKeys = 2 * kPage;
 // Even numbers of stages: the even and the odd steps have their own copy warp, MMA thread and
 // softmax warps, which run ahead of one another, so each keeps to its own stages (a wait by parity
 // of a stage that both used would take the use before last for the last).
-constexpr int kCodeStages = 4, kKeyStages = 4, kScoreStages = 2, kMeta = 16;
+constexpr int kCodeStages = 4, kKeyStages = 2, kScoreStages = 2, kMeta = 16;
 static_assert(kCodeStages % 2 == 0 && kKeyStages % 2 == 0 && kScoreStages % 2 == 0, "stages by parity of the step");
 // a step's record lives until its sums are done: the copies run at most the sum of the stages ahead
 static_assert(kMeta >= kCodeStages + kKeyStages + kScoreStages + 2, "records outlive their steps");
@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
             const WinStep m = sm.meta[i % kMeta];
             const uint32_t tm = tmem + 128u * ss + ((uint32_t)((warp & 3) * 32) << 16);
             const int rr = m.row0 + row, pos0 = m.L - m.n, pos = pos0 + rr / G;
-            float *dst = p.lse + ((int64_t)(m.c0 + rr / G) * p.num_q_heads + m.h * G + rr % G) * p.max_blocks + m.j;
+            const int64_t row_step = (int64_t)m.n * p.num_q_heads;  // from a page's sums to the next one's
+            float *dst = pw_sums(p, PwSeq{m.c0, m.n, m.L}) + m.j * row_step + (int64_t)m.h * (m.n * G) + rr;
 #pragma unroll
             for (int hh = 0; hh < 2; hh++) {
                 uint32_t x[2][32];
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kWinThreads, 1) page_window_kernel(PageWeights
                 }
                 float la, lb;
                 upk2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), la, lb);
-                if (hh < m.pages && rr < m.n * G) dst[hh] = f * mx + __log2f(la + lb);
+                if (hh < m.pages && rr < m.n * G) dst[hh * row_step] = f * mx + __log2f(la + lb);
             }
         }
     } else if (warp < 2) {
