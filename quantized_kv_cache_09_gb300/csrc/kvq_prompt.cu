@@ -21,8 +21,8 @@
 //             M = N = 128.  (An MMA holds its issuer until the tensor pipe takes it,
 //             and a wait between MMAs costs ~100 cycles: with one thread for both
 //             tiles the pipe was busy 49% of the time.)
-//   1         walks the unit list and issues the copies of K and V (TMA) into a
-//             ring of four 32 KB stages.
+//   1         takes units, tells the other roles and issues the copies of K and V
+//             (TMA) into a ring of four 32 KB stages.
 //   3         issues the copies of the Q tiles.  The last step(s) of a unit hold
 //             keys past some row's position: of their V this warp zeroes the rows
 //             past the sequence's end and takes out values that are not finite
@@ -40,19 +40,22 @@
 // Without the order both tiles' softmaxes fall together and the pipe idles (16384
 // tokens x 64 heads: 3.8 ms against 2.9).
 //
-// Measured (GB300): 16384 tokens x 64 / 8 heads 2.9 ms alone, 3.06 ms back to
-// back at the power cap (1.44 - 1.52 PFLOP/s, 0.75 - 0.79 of the measured bf16
-// rate); 8 x 2048 tokens x 32 heads 268 us (1.03 PFLOP/s), where a unit has 8.5
-// steps: its first and last steps, O's way out and the turn between units cost
-// about as much as three of them.  A steady step of both tiles takes ~2900 cycles
-// for 2048 of MMAs: half as many loads or no exponentials at all gain 4% each.
+// Measured (GB300): 16384 tokens x 64 / 8 heads 2.9 ms alone, 3.0 - 3.1 ms back to
+// back at the power cap (1.42 - 1.52 PFLOP/s, 0.74 - 0.79 of the measured bf16
+// rate); 8 x 2048 tokens x 32 heads 248 - 265 us (1.04 - 1.11 PFLOP/s), where a unit
+// has 8.5 steps: its first and last steps, O's way out and the turn between units
+// cost about as much as two of them.  A steady step of both tiles takes ~2900 - 3300
+// cycles for 2048 of MMAs: half as many loads or no exponentials at all gain 4% each.
 //
 // Unit order: cache heads in groups whose keys and values fit half of L2, since
-// each level reads them again (8 x 2048 x 32 heads, 268 MB of them: 265 us, 282
-// without groups, 284 with groups of 32 or 96 MB); of a group by the number of the unit in
-// its sequence, the highest (most keys) first, over sequences and heads, dealt
-// to the CTAs forwards and backwards in turn -- longest first without a counter
-// to fetch from.
+// each level reads them again (8 x 2048 x 32 heads, 268 MB of them, inputs warm:
+// 250 us; 263 with groups of 48 MB, 258 with 128 MB); of a group by the number of
+// the unit in its sequence, the highest (most keys) first, over sequences and heads.
+// Units go to the CTAs as they come free: the grid has a CTA for each (16 per SM at
+// most, then a ticket is several units), and one that runs takes the places of those
+// that have not started.  Dealt in a fixed order, forwards and backwards in turn, the
+// busiest CTA had 4% (8 x 2048) to 6% (16 prompts of 65 .. 8192 tokens) more steps than
+// the mean: 16 prompts 858 us, 826 so; 24 of 50 .. 4000 tokens 1150, 1110.
 #include <cuda.h>
 
 #include <type_traits>
@@ -80,8 +83,9 @@ constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 // a softmax scale of 0 scores 1e-38 * raw instead, so that a masked score stays -inf
 constexpr float kMinScale = 1.17549435e-38f;
-// registers per thread after the split: 2 * 176 + 104 + 56 = 4 * 128, the launch's
-constexpr int kRegsSoftmax = 176, kRegsEpilogue = 104, kRegsIssue = 56;
+// registers per thread after the split: 2 * 184 + 80 + 64 = 4 * 128, the launch's (nothing is
+// spilled; with 176, 104 and 56 the spills cost 7%)
+constexpr int kRegsSoftmax = 184, kRegsEpilogue = 80, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + kRegsEpilogue + kRegsIssue <= 4 * (65536 / kPromptThreads), "register split");
 
 template <int N>
@@ -147,7 +151,9 @@ struct alignas(1024) PromptSmem {
     uint64_t o_free[kUnitTiles];   // O and ml read by the epilogue
     uint64_t ml_full[kUnitTiles];  // a unit's maxima and sums written
     uint64_t unit_full[2], unit_free[2];
+    uint64_t ticket_full;
     uint64_t mma_done;
+    uint4 ticket;  // the answer to a request for one
     float2 ml[kUnitTiles][kTileRows];
     PromptUnit unit[2];
     uint32_t wild[4];  // by unit: some value of a mixed step is not finite (warp 3 may be two units ahead)
@@ -209,6 +215,30 @@ __device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
+// Take the place of a CTA of this grid that has not started: the answer (16 bytes) comes to `dst`.
+__device__ __forceinline__ void ask_ticket(uint4 *dst, uint64_t *bar)
+{
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_addr(dst)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// Its block index, or -1: every CTA has started (and no further request may be made).
+__device__ __forceinline__ int read_ticket(const uint4 *src)
+{
+    int id;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%1];\n\tmov.b32 %0, -1;\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(id)
+        : "r"(smem_addr(src))
+        : "memory");
+    return id;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float d;
@@ -256,6 +286,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             mbar_init(&sm.unit_full[s], 1);
             mbar_init(&sm.unit_free[s], 15);  // 8 softmax warps, 4 epilogue warps, 2 MMA threads, warp 3
         }
+        mbar_init(&sm.ticket_full, 1);
         mbar_init(&sm.mma_done, 2);
         mbar_init_fence();
     }
@@ -589,87 +620,140 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
         } else if (warp == 1) {
             // ---- units and copies ----
             const int H = p.num_heads, ut = p.unit_tokens;
-            // a sequence's length, 0 where its bounds are broken
+            // a sequence's length, -1 where its bounds are broken
             auto length = [&](int b) {
                 const int c0 = p.cu[b], n = p.cu[b + 1] - c0;
-                const bool good = n >= 0 && n <= p.max_n && c0 >= 0 && (int64_t)c0 + n <= p.total;
-                if (!good && blockIdx.x == 0) set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
-                return good ? n : 0;
+                return n >= 0 && n <= p.max_n && c0 >= 0 && (int64_t)c0 + n <= p.total ? n : -1;
             };
-            const bool few = p.num_seqs <= 32;  // lengths stay in registers
+            const bool few = p.num_seqs <= 32;  // lengths and first rows stay in registers
             const int mine = few && lane < p.num_seqs ? length(lane) : 0;
+            const int mine_c0 = few && lane < p.num_seqs ? p.cu[lane] : 0;
             // sequences (of 32 from b0 on) with a unit number x, as a mask
             auto longer = [&](int b0, int x) {
                 const int n = few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0;
                 return __ballot_sync(kFull, n > (int64_t)x * ut);
             };
-            auto level = [&](int x) {
-                int c = 0;
-#pragma unroll 1
-                for (int b0 = 0; b0 < p.num_seqs; b0 += 32) c += __popc(longer(b0, x));
-                return c;
-            };
             int longest = 0;
-            int64_t tokens = 0;
+            int64_t tokens = 0, units = 0;
 #pragma unroll 1
             for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
                 const int n = few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0;
+                if (n < 0) set_flag(p.status, KVQ_FLAG_BAD_LENGTH);
                 longest = max(longest, n);
-                tokens += n;
+                tokens += max(n, 0);
+                units += (max(n, 0) + (int64_t)ut - 1) / ut * H;
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(kFull, tokens, o);
-            const int top = (__reduce_max_sync(kFull, longest) + ut - 1) / ut - 1;
+            for (int o = 16; o > 0; o >>= 1) {
+                tokens += __shfl_xor_sync(kFull, tokens, o);
+                units += __shfl_xor_sync(kFull, units, o);
+            }
+            const int top = (int)((__reduce_max_sync(kFull, longest) + (int64_t)ut - 1) / ut) - 1;
             // heads go in groups whose K and V stay in L2 while all levels read them
             const int64_t groups = (tokens * H * (kHeadDim * 4) + kGroupBytes - 1) / kGroupBytes;
             const int hg = groups > H ? 1 : groups > 1 ? (int)((H + groups - 1) / groups) : H;
-            int x = top, h0 = top < 0 ? H : 0, hn = hg;
-            int64_t base = 0;      // units before level x of the heads from h0 on
-            int count = level(x);  // sequences on level x
+            int x = top, h0 = 0, hn = hg;
+            int64_t base = 0;        // units before level x of the heads from h0 on
+            int count = 0, same = 0;  // sequences on level x; the last level with as many
             int at = 0, passed = 0;  // of the level's: `passed` come before sequence `at`, a multiple of 32
-            Ring ring;
-            uint32_t used = 0;  // stages filled so far, up to kStages
-            // bit s: parity of stage s's next kv_full, kv_raw; whether its last fill was a mixed V
-            uint32_t full_phase = 0, raw_phase = 0, last_raw = 0;
-            for (int r = 0;; r++) {
-                const int64_t id = (int64_t)r * gridDim.x + (r & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                while (h0 < H && id >= base + (int64_t)count * hn) {
-                    base += (int64_t)count * hn;
-                    if (--x < 0) {
+            auto enter = [&](int x) {
+                int c = 0, below = 0;  // the longest sequence without a unit x
+#pragma unroll 1
+                for (int b0 = 0; b0 < p.num_seqs; b0 += 32) {
+                    const int n = few ? mine : b0 + lane < p.num_seqs ? length(b0 + lane) : 0;
+                    const bool on = n > (int64_t)x * ut;
+                    c += __popc(__ballot_sync(kFull, on));
+                    below = max(below, on ? 0 : n);
+                }
+                below = __reduce_max_sync(kFull, below);
+                count = c;
+                same = (int)((below + (int64_t)ut - 1) / ut);
+                at = passed = 0;
+            };
+            if (units > 0) enter(x);
+            // the unit of number `id`, a negative length behind the last one
+            auto find = [&](int64_t id) {
+                PromptUnit u = {0, -1, 0, 0};
+                if (id >= units) return u;
+                if (id < base) {  // (numbers come in order, as a rule: the search goes on where the last one ended)
+                    base = 0;
+                    h0 = 0;
+                    hn = hg;
+                    x = top;
+                    enter(x);
+                }
+                while (id >= base + (int64_t)count * hn) {
+                    const int64_t size = (int64_t)count * hn, past = (id - base) / size;
+                    const int levels = x - same + 1, go = past < levels ? (int)past : levels;
+                    base += go * size;
+                    x -= go;
+                    if (x < 0) {
                         h0 += hg;
                         hn = min(hg, H - h0);
                         x = top;
                     }
-                    count = level(x);
-                    at = passed = 0;
+                    enter(x);
                 }
-                PromptUnit u = {0, -1, 0, 0};
-                if (h0 < H) {
-                    const uint32_t rank = (uint32_t)(id - base);  // (at most 65535 sequences x 65535 heads)
-                    const int k = (int)(rank / (uint32_t)hn);     // the k-th sequence of the level
-                    u.h = h0 + (int)(rank % (uint32_t)hn);
-                    // (its units come in order: the search goes on where the last one ended)
-                    uint32_t m = longer(at, x);
+                const uint32_t rank = (uint32_t)(id - base);  // (at most 65535 sequences x 65535 heads)
+                const int k = (int)(rank / (uint32_t)hn);     // the k-th sequence of the level
+                u.h = h0 + (int)(rank % (uint32_t)hn);
+                if (k < passed) at = passed = 0;
+                uint32_t m = longer(at, x);
 #pragma unroll 1
-                    while (k >= passed + __popc(m) && at + 32 < p.num_seqs) {
-                        passed += __popc(m);
-                        at += 32;
-                        m = longer(at, x);
-                    }
+                while (k >= passed + __popc(m) && at + 32 < p.num_seqs) {
+                    passed += __popc(m);
+                    at += 32;
+                    m = longer(at, x);
+                }
 #pragma unroll 1
-                    for (int skip = k - passed; skip > 0; skip--) m &= m - 1u;
-                    const int b = min(at + max(__ffs(m) - 1, 0), p.num_seqs - 1);
+                for (int skip = k - passed; skip > 0; skip--) m &= m - 1u;
+                const int b = min(at + max(__ffs(m) - 1, 0), p.num_seqs - 1);
+                if (few) {
+                    u.c0 = __shfl_sync(kFull, mine_c0, b);
+                    u.n = __shfl_sync(kFull, mine, b);
+                } else {
                     u.c0 = p.cu[b];
                     u.n = p.cu[b + 1] - u.c0;
-                    u.tok0 = x * ut;
                 }
+                u.tok0 = x * ut;
+                return u;
+            };
+            // the r-th unit of this CTA to the other roles
+            auto publish = [&](int r, const PromptUnit &u) {
                 ok = __all_sync(kFull, r < 2 || mbar_wait_short(&sm.unit_free[r & 1], (uint32_t)((r >> 1) - 1) & 1u));
-                if (!ok) break;
-                if (lane == 0) {
+                if (lane == 0 && ok) {
                     sm.unit[r & 1] = u;
                     mbar_arrive(&sm.unit_full[r & 1]);
                 }
-                if (u.n < 0) break;
+            };
+            // a ticket is `per` units; this CTA's own first, then those of CTAs that have not started
+            const int64_t per = (units + gridDim.x - 1) / gridDim.x;
+            int64_t id = (int64_t)blockIdx.x * per;
+            int left = (int)per;  // of the ticket, with this one
+            uint32_t asked = 0, answered = 0;
+            bool more = true;  // no refusal yet
+            auto ask = [&]() {
+                __syncwarp();  // (the last answer was read)
+                if (lane == 0) ask_ticket(&sm.ticket, &sm.ticket_full);
+                asked++;
+            };
+            auto answer = [&]() {
+                const bool came = __all_sync(kFull, mbar_wait_short(&sm.ticket_full, answered++ & 1u));
+                const int t = came ? read_ticket(&sm.ticket) : -1;
+                if (!came) ok = false;
+                more = t >= 0;
+                return t;
+            };
+            Ring ring;
+            uint32_t used = 0;  // stages filled so far, up to kStages
+            // bit s: parity of stage s's next kv_full, kv_raw; whether its last fill was a mixed V
+            uint32_t full_phase = 0, raw_phase = 0, last_raw = 0;
+            PromptUnit u = find(id);
+            for (int r = 0;; r++) {
+                publish(r, u);
+                if (!ok || u.n < 0) break;
+                const bool last = left == 1 || id + 1 >= units;  // of the ticket
+                if (last && more) ask();
                 if (lane == 0) {
                     const Span sp(u, p);
                     auto stage = [&](const CUtensorMap *map, int key, bool raw) {
@@ -698,6 +782,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 }
                 ok = __all_sync(kFull, ok);
                 if (!ok) break;
+                id++;
+                left--;
+                if (last) {
+                    const int t = more ? answer() : -1;
+                    id = t < 0 ? units : t * per;
+                    left = (int)per;
+                }
+                u = find(id);
+            }
+            if (asked != answered) answer();  // (after a failed wait: none is on its way when the CTA ends)
+            // the tickets behind the last unit, or each would start a CTA
+            while (ok && more) {
+                ask();
+                answer();
             }
             if (lane == 0) {  // no copy in flight when the CTA ends
                 for (uint32_t s = 0; s < used; s++) {
@@ -839,11 +937,12 @@ cudaError_t launch_prompt_type(const PromptParams &p, const uint16_t *q, int64_t
     auto kernel = p.score_scale < 0.0f ? prompt_attn_kernel<BF, true> : prompt_attn_kernel<BF, false>;
     const cudaError_t e = allow_smem(kernel, sizeof(PromptSmem), done[p.score_scale < 0.0f]);
     if (e != cudaSuccess) return e;
-    // at most one CTA per SM, and no more than there can be units
+    // a CTA for every unit there can be, up to 32 per SM (then a ticket is several units): the first
+    // ones to run take the others' places
     const int64_t ut = p.unit_tokens;
     const int64_t by_max = (int64_t)p.num_seqs * ((p.max_n + ut - 1) / ut), by_total = p.total / ut + p.num_seqs;
     const int64_t units = (by_max < by_total ? by_max : by_total) * p.num_heads;
-    const int grid = units < num_sms ? (int)units : num_sms;
+    const int64_t most = 16 * (int64_t)num_sms, grid = units < most ? units : most;
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(kPromptThreads), sizeof(PromptSmem), s, p,
                         mq, mk, mv);
 }

@@ -138,6 +138,21 @@ def test_thousands_of_short_prompts(cuda_ok):
     _check(*_inputs(lens, 2, 2, torch.float16, seed=14))
 
 
+def test_few_rows_in_a_large_buffer(cuda_ok):
+    """Bounds that allow for many more units than there are: the buffers of a captured step, for instance."""
+    for lens in ([5, 0, 130, 1], [0, 0], [300]):
+        _check(*_inputs(lens, 4, 4, torch.bfloat16, seed=15, pad=40000), max_n=40000)
+
+
+def test_units_of_very_different_lengths(cuda_ok):
+    """More units than SMs, long and short: which CTA has one depends on timing, the bits do not."""
+    lens = [1900, 3, 640, 1, 129, 2500, 77, 300]
+    q, k, v, cu = _inputs(lens, 8, 8, torch.float16, seed=16)
+    want = _check(q, k, v, cu)
+    for _ in range(3):
+        assert torch.equal(_run(q, k, v, cu)[0], want)
+
+
 def test_without_lse_and_repeatable(cuda_ok):
     q, k, v, cu = _inputs([600, 128], 8, 1, torch.float16, seed=8)
     want, _, _ = _run(q, k, v, cu)
