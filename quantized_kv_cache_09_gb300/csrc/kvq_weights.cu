@@ -25,7 +25,10 @@
 // 32K tokens x 32 heads int4 (1.04 GB) 168 us, 0.92 of the measured copy rate;
 // 32 x 8K x 8 heads FP8 with 8 query heads each (250 MB) 45 us, 0.83; 8 x 8193 x
 // 32 heads int4 (134 MB) 30 us, 0.67 -- a launch begins and ends in about 8 us --
-// plus 6 - 12 us of page_sum_kernel.  16 warps with a ring of three 4 KB copies
+// plus 2 - 4 us of page_sum_kernel (8 us, with page_join_kernel, for the 1024 rows of a
+// window of 32 tokens).  The log2-sums lie [page][row]: a row sum reads 256 bytes of 64
+// rows at once and the writers of a tile of rows lie side by side (laid out [row][page],
+// windows of 32 tokens took 46 us against 38).  16 warps with a ring of three 4 KB copies
 // each: 12 warps with four 57 us on 268 MB against 51, 18 with three 57.
 #include "kvq_weights.cuh"
 

@@ -22,9 +22,10 @@
 // Every hand-off is an mbarrier, every wait bounded.
 //
 // Measured: the last 32 tokens of 16 prompts of 512 .. 16384 tokens, int8, 32 / 8 heads (20 GFLOP,
-// 84 MB): 38 us (mma.sync with 16 rows a unit, which widens each page eight times: 116 us).  A step
-// takes ~1500 cycles, of which the tensor pipe and the exponentials need ~512 each: the softmax
-// warps of both parities run together and hold S meanwhile.  Rows: 17 fill a tile of 128 as 128 do;
+// 84 MB): 30 us (mma.sync with 16 rows a unit, which widens each page eight times: 116 us).  A step
+// takes ~1350 cycles, of which the tensor pipe and the exponentials need ~512 each; without any
+// softmax, widening and all but one MMA of a step it still takes ~900, the hand-offs from role to
+// role.  (Letting S go page by page: 6% slower.)  Rows: 17 fill a tile of 128 as 128 do;
 // up to 16 rows page_lse_kernel reads the codes at the rate of HBM.
 #include "kvq_tc.cuh"
 #include "kvq_weights.cuh"
@@ -38,7 +39,8 @@ constexpr int kWinRows = 128;
 constexpr int kWinKeys = 2 * kPage;
 // Even numbers of stages: the even and the odd steps have their own copy warp, MMA thread and
 // softmax warps, which run ahead of one another, so each keeps to its own stages (a wait by parity
-// of a stage that both used would take the use before last for the last).
+// of a stage that both used would take the use before last for the last).  Two widened tiles: with
+// four, the widening runs ahead and takes the sums' issue slots (33 us against 29).
 constexpr int kCodeStages = 4, kKeyStages = 2, kScoreStages = 2, kMeta = 16;
 static_assert(kCodeStages % 2 == 0 && kKeyStages % 2 == 0 && kScoreStages % 2 == 0, "stages by parity of the step");
 // a step's record lives until its sums are done: the copies run at most the sum of the stages ahead
