@@ -55,7 +55,9 @@
 // most, then a ticket is several units), and one that runs takes the places of those
 // that have not started.  Dealt in a fixed order, forwards and backwards in turn, the
 // busiest CTA had 4% (8 x 2048) to 6% (16 prompts of 65 .. 8192 tokens) more steps than
-// the mean: 16 prompts 858 us, 826 so; 24 of 50 .. 4000 tokens 1150, 1110.
+// the mean: 16 prompts 858 us, 829 so; 24 of 50 .. 4000 tokens 1145, 1085; 6 of 150 .. 2000
+// x 32 / 32 heads 76, 72; against 980, 1065 where a ticket is six units (150 of 10 .. 1200
+// tokens x 32 / 32 heads).
 #include <cuda.h>
 
 #include <type_traits>
@@ -675,12 +677,17 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             auto find = [&](int64_t id) {
                 PromptUnit u = {0, -1, 0, 0};
                 if (id >= units) return u;
-                if (id < base) {  // (numbers come in order, as a rule: the search goes on where the last one ended)
-                    base = 0;
-                    h0 = 0;
-                    hn = hg;
-                    x = top;
+                // (numbers come nearly in order: the search goes on where the last one ended, a few levels back at most)
+                while (id < base) {
+                    if (x == top) {
+                        h0 -= hg;
+                        hn = hg;
+                        x = 0;
+                    } else {
+                        x++;
+                    }
                     enter(x);
+                    base -= (int64_t)count * hn;
                 }
                 while (id >= base + (int64_t)count * hn) {
                     const int64_t size = (int64_t)count * hn, past = (id - base) / size;
@@ -730,13 +737,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
             const int64_t per = (units + gridDim.x - 1) / gridDim.x;
             int64_t id = (int64_t)blockIdx.x * per;
             int left = (int)per;  // of the ticket, with this one
-            uint32_t asked = 0, answered = 0;
+            uint32_t answered = 0;
             bool more = true;  // no refusal yet
-            auto ask = [&]() {
-                __syncwarp();  // (the last answer was read)
-                if (lane == 0) ask_ticket(&sm.ticket, &sm.ticket_full);
-                asked++;
-            };
             auto answer = [&]() {
                 const bool came = __all_sync(kFull, mbar_wait_short(&sm.ticket_full, answered++ & 1u));
                 const int t = came ? read_ticket(&sm.ticket) : -1;
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                 publish(r, u);
                 if (!ok || u.n < 0) break;
                 const bool last = left == 1 || id + 1 >= units;  // of the ticket
-                if (last && more) ask();
+                const bool take = last && more;
                 if (lane == 0) {
                     const Span sp(u, p);
                     auto stage = [&](const CUtensorMap *map, int key, bool raw) {
@@ -775,26 +777,29 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
                     };
 #pragma unroll 1
                     for (int i = 0; i < sp.total && ok; i++) {
+                        // (an answer takes 1 - 2 us: asked for as late as the copies' waits cover it, so that a CTA
+                        // takes a unit about when it is free)
+                        if (take && i == max(sp.total - 2, 0)) ask_ticket(&sm.ticket, &sm.ticket_full);
 #pragma unroll 1
                         for (int kv = 0; kv < 2 && ok; kv++)
                             stage(kv == 0 ? &map_k : &map_v, i * kKeys, kv == 1 && i >= sp.mixed);
                     }
                 }
                 ok = __all_sync(kFull, ok);
-                if (!ok) break;
+                if (!ok) break;  // (flagged; the answer, if one is on its way, comes long before the other waits run out)
                 id++;
                 left--;
                 if (last) {
-                    const int t = more ? answer() : -1;
+                    const int t = take ? answer() : -1;
                     id = t < 0 ? units : t * per;
                     left = (int)per;
                 }
                 u = find(id);
             }
-            if (asked != answered) answer();  // (after a failed wait: none is on its way when the CTA ends)
             // the tickets behind the last unit, or each would start a CTA
             while (ok && more) {
-                ask();
+                __syncwarp();  // (the last answer was read)
+                if (lane == 0) ask_ticket(&sm.ticket, &sm.ticket_full);
                 answer();
             }
             if (lane == 0) {  // no copy in flight when the CTA ends

@@ -153,6 +153,12 @@ def test_units_of_very_different_lengths(cuda_ok):
         assert torch.equal(_run(q, k, v, cu)[0], want)
 
 
+def test_many_sequences_of_many_lengths(cuda_ok):
+    """Levels of few units each, in several groups of heads: units come out of order by more than a level."""
+    lens = [1 + (i * 97) % 1210 for i in range(150)]
+    _check(*_inputs(lens, 12, 12, torch.float16, seed=17))
+
+
 def test_without_lse_and_repeatable(cuda_ok):
     q, k, v, cu = _inputs([600, 128], 8, 1, torch.float16, seed=8)
     want, _, _ = _run(q, k, v, cu)
